@@ -113,7 +113,9 @@ typedef struct CUstream_st *cudaStream_t;
 #define DFX_STATUS_HEADER 0x1u  /* header disagrees with the plan or the buffer size */
 #define DFX_STATUS_TABLE 0x2u   /* code lengths above 24 or Kraft sum not exactly 1
                                    (coder 1: frequencies not summing to 2^table_log) */
-#define DFX_STATUS_INDEX 0x4u   /* group start bits or chunk lengths inconsistent */
+#define DFX_STATUS_INDEX 0x4u   /* group start bits or chunk lengths inconsistent; a row, slot or
+                                   expert offset outside its tensor (dfx_quantize_fp8,
+                                   dfx_combine, dfx_gemm_fp8) */
 #define DFX_STATUS_STREAM 0x8u  /* a bit pattern that is no code, or a chunk that
                                    did not consume exactly its stated length */
 #define DFX_STATUS_TIMEOUT 0x10u /* a copy into shared memory did not complete within the
@@ -292,6 +294,8 @@ int dfx_device_status(dfx_plan_t plan, cudaStream_t stream, uint32_t *h_status);
  * in flight.  flags = 0 restores normal decoding.  Process-wide, not for
  * concurrent use; unknown flags return DFX_ERR_ARG. */
 #define DFX_INJECT_SKIP_SLICE_COPY 0x1u
+/* The same for dfx_gemm_fp8: every later call leaves out each CTA's first tile copies. */
+#define DFX_INJECT_SKIP_TILE_COPY 0x4u
 int dfx_debug_inject(uint32_t flags);
 
 /* Release the plan and its device status word.  NULL is accepted. */
@@ -317,6 +321,117 @@ int dfx_free(dfx_plan_t plan);
  * the same bytes as dfx_encode. */
 int dfx_encode_static(const void *d_bf16, uint64_t n, const dfx_params *params, void *d_out,
                       size_t out_capacity, size_t *h_compressed_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Products with 8-bit weights, and the layers of experts they serve.
+ *
+ * Weights restored by dfx_decode can be laid out once more, in 8 bits, for products of any
+ * number of tokens: dfx_quantize_fp8 turns BF16 (or FP32) values into e4m3 with a scale for
+ * each block of 128, dfx_gemm_fp8 multiplies such operands on the tensor cores.  With several
+ * weight matrices (experts) dfx_route chooses each token's experts and sorts the assignments
+ * by expert, dfx_quantize_fp8 gathers the tokens in that order, dfx_gemm_fp8 multiplies each
+ * expert's rows by its own matrix, and dfx_combine brings the results back, weighted.  This
+ * form is lossy; the container is not, and stays the stored one.
+ *
+ * The 8-bit form: values are e4m3 bytes, rows `ld` bytes apart (a multiple of 16); scales are
+ * e8m0 bytes (2^(byte - 127)), one per 128 values of a row (the last block of a row may be
+ * shorter), rows of scales `ld_scales` bytes apart (a multiple of 4, and a buffer holds whole
+ * rows of ld_scales bytes).  The bytes of a row behind its last value or scale are neither
+ * read for their value nor written.
+ *
+ * Each call takes a plan of the current device: its n and parameters play no part, its status
+ * word receives what only the GPU can see (below).  All buffers are device memory, 16-byte
+ * aligned; every call is asynchronous, allocates nothing and can be captured into a graph. */
+#define DFX_F32 0u
+#define DFX_BF16 1u
+
+#define DFX_SCORE_SOFTMAX 0u
+#define DFX_SCORE_SIGMOID 1u
+
+typedef struct {
+    uint32_t score;       /* DFX_SCORE_SOFTMAX or DFX_SCORE_SIGMOID */
+    uint32_t topk;        /* experts per token, 1..32, at most `experts` */
+    uint32_t groups;      /* 0 or 1: none; else equal runs of neighbouring experts, at most 32 */
+    uint32_t top_groups;  /* groups a token may choose from, 1..groups */
+    uint32_t group_best;  /* a group's score: its best choice (1, or 0) or its best two's sum (2) */
+    uint32_t renormalize; /* 1: a token's weights are divided by their sum */
+    float scale;          /* factor of every weight (0 -> 1) */
+} dfx_route_params;
+
+/* Bytes of workspace dfx_route needs for its assignment lists.  Host only, no CUDA call. */
+int dfx_route_workspace(uint64_t tokens, uint32_t experts, const dfx_route_params *params, size_t *bytes);
+
+/* Each token's best experts, their weights, and the assignments sorted by expert.
+ * Score of expert e: softmax over the token's logits, or 1 / (1 + exp(-logit)).  Choices go by
+ * score + bias (bias NULL: by score), first among groups, then among the experts of the best
+ * top_groups groups; ties go to the lowest index; weights are the scores without the bias.
+ * An expert whose logit (or bias) is -inf or NaN is closed to the token: its score is 0 and it
+ * is never chosen.  A token with fewer than topk experts to choose from (none, if it is
+ * padding with every logit -inf) has -1 and weight 0 in the places left over.  If the chosen
+ * scores sum to 0, renormalised weights are 0.
+ *   d_logits, logits_type, ld_logits: tokens x experts, DFX_F32 or DFX_BF16, rows ld_logits
+ *     elements apart; experts <= 512 (else DFX_ERR_UNSUPPORTED).  d_bias: NULL or FP32[experts].
+ *   d_ids, d_weights: tokens x topk, best first.
+ *   d_offsets: int32[experts + 1]; d_rows: int32[tokens * topk]; d_slots: int32[tokens x topk];
+ *     or all NULL.  The assignments of expert e have the slots offsets[e] .. offsets[e + 1] - 1
+ *     in the order of their tokens; rows[slot] is the token, slots[t, k] the slot of a token's
+ *     k-th expert (-1: none).  rows[] behind the last assignment are -1.
+ *   d_workspace: scratch for the lists, workspace_bytes >= dfx_route_workspace's (not needed
+ *     without them); calls that may overlap need one each.
+ * tokens * topk < 2^31, else DFX_ERR_TOO_LARGE.  One launch up to 64 tokens, else two. */
+int dfx_route(dfx_plan_t plan, const void *d_logits, uint32_t logits_type, uint64_t ld_logits, uint64_t tokens,
+              uint32_t experts, const float *d_bias, const dfx_route_params *params, int32_t *d_ids, float *d_weights,
+              int32_t *d_offsets, int32_t *d_rows, int32_t *d_slots, void *d_workspace, size_t workspace_bytes,
+              cudaStream_t stream);
+
+/* e4m3 and block scales of a matrix of `rows` x `cols` values.
+ * A block is 128 neighbouring values of a row (block_rows = 1: activations) or 128 x 128 values
+ * (block_rows = 128: weights).  Its scale is the smallest power of two that brings its largest
+ * finite magnitude to 448 or below (at least 2^-127; 1 for a block of zeros); value / scale is
+ * rounded once, to nearest even.  NaN and infinities become NaN.
+ *   d_x, x_type, ld_x: x_rows rows, DFX_F32 or DFX_BF16, ld_x elements apart.
+ *   d_index: NULL, or int32[rows]: output row r is row index[r] of x.  A negative index leaves
+ *     row r as it was; one of x_rows or more does too, and sets DFX_STATUS_INDEX.  NULL needs
+ *     rows <= x_rows.
+ *   flags: DFX_QUANT_SWIGLU: a row of x holds cols gates, then cols values, and
+ *     gate / (1 + exp(-gate)) * value is quantized (in FP32, without a rounding in between).
+ *   d_q, ld_q: rows x cols bytes; d_scales, ld_scales: ceil(rows / block_rows) x ceil(cols / 128).
+ * d_index and flags go with block_rows = 1 only (else DFX_ERR_UNSUPPORTED). */
+#define DFX_QUANT_SWIGLU 0x1u
+int dfx_quantize_fp8(dfx_plan_t plan, const void *d_x, uint32_t x_type, uint64_t ld_x, uint64_t x_rows,
+                     const int32_t *d_index, uint64_t rows, uint64_t cols, uint32_t block_rows, uint32_t flags,
+                     void *d_q, uint64_t ld_q, void *d_scales, uint64_t ld_scales, cudaStream_t stream);
+
+/* Y = X W^T of 8-bit operands: Y[t, r] = sum over the blocks b of
+ * x_scale[t, b] w_scale[r / 128, b] sum over k in b of x[t, k] w[r, k], accumulated in FP32 on
+ * the tensor cores (tcgen05.mma takes the scales with the values) in an order of the hardware's
+ * choosing, and rounded once, to y_type.
+ *   d_x, ld_x, d_x_scales, ld_x_scales: tokens x cols, blocks of 1 x 128.
+ *   d_w, ld_w, d_w_scales, ld_w_scales: experts matrices of rows x cols, blocks of 128 x 128, one
+ *     behind the other: matrix e starts at row e * rows of d_w, and at row
+ *     e * ceil(rows / 128) of d_w_scales.
+ *   d_offsets: int32[experts + 1], not decreasing, within 0..tokens: the rows
+ *     offsets[e] .. offsets[e + 1] - 1 of X are multiplied by matrix e.  Rows outside them are
+ *     not computed, and their rows of Y stay as they were.  NULL with experts = 1: every row.
+ *     An offset out of order or range is clamped and sets DFX_STATUS_INDEX.
+ *   d_y, y_type, ld_y: tokens x rows, DFX_F32 or DFX_BF16, ld_y elements apart; the elements of
+ *     a row behind `rows` stay as they were.
+ * experts <= 1024 (else DFX_ERR_UNSUPPORTED); tokens and experts * rows < 2^31 (else
+ * DFX_ERR_TOO_LARGE).  A wait inside the kernel that runs out sets DFX_STATUS_TIMEOUT (Y is then
+ * not valid).  One launch. */
+int dfx_gemm_fp8(dfx_plan_t plan, const void *d_x, uint64_t ld_x, const void *d_x_scales, uint64_t ld_x_scales,
+                 uint64_t tokens, const void *d_w, uint64_t ld_w, const void *d_w_scales, uint64_t ld_w_scales,
+                 uint64_t rows, uint64_t cols, uint32_t experts, const int32_t *d_offsets, void *d_y, uint32_t y_type,
+                 uint64_t ld_y, cudaStream_t stream);
+
+/* y[t] = sum over k of weights[t, k] z[slots[t, k]], added in the order of k in FP32 and rounded
+ * once.  A negative slot adds nothing (a token with none gets zeros); one of z_rows or more adds
+ * nothing and sets DFX_STATUS_INDEX.
+ *   d_z, z_type, ld_z: z_rows x cols; d_slots, d_weights: tokens x topk (topk <= 32);
+ *   d_y, y_type, ld_y: tokens x cols.  Types DFX_F32 or DFX_BF16. */
+int dfx_combine(dfx_plan_t plan, const void *d_z, uint32_t z_type, uint64_t ld_z, uint64_t z_rows, uint64_t cols,
+                const int32_t *d_slots, const float *d_weights, uint64_t tokens, uint32_t topk, void *d_y,
+                uint32_t y_type, uint64_t ld_y, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

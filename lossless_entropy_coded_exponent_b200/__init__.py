@@ -29,10 +29,16 @@ DFX_STATUS_INDEX = 0x4
 DFX_STATUS_STREAM = 0x8
 DFX_STATUS_TIMEOUT = 0x10
 DFX_INJECT_SKIP_SLICE_COPY = 0x1
+DFX_INJECT_SKIP_TILE_COPY = 0x4
 DFX_CODER_HUFFMAN = 0
 DFX_CODER_TANS = 1
 DFX_CODER_TANS2 = 2  # tANS with two interleaved states per chunk
 DFX_DECODE_EARLY_READ = 0x1
+DFX_F32 = 0
+DFX_BF16 = 1
+DFX_SCORE_SOFTMAX = 0
+DFX_SCORE_SIGMOID = 1
+DFX_QUANT_SWIGLU = 0x1
 
 # The exported C symbols, in include/dfx.h order.
 EXPORTS = (
@@ -50,6 +56,11 @@ EXPORTS = (
     "dfx_free",
     "dfx_encode_static",
     "dfx_debug_inject",
+    "dfx_route_workspace",
+    "dfx_route",
+    "dfx_quantize_fp8",
+    "dfx_gemm_fp8",
+    "dfx_combine",
 )
 
 
@@ -68,6 +79,12 @@ class dfx_layout(ctypes.Structure):
     _fields_ = [(name, ctypes.c_uint64) for name in
                 ("n", "n_chunk", "n_group", "off_len", "off_gbase", "off_clen", "off_m", "off_stream",
                  "stream_bytes", "total_bytes")]
+
+
+class dfx_route_params(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_uint32), ("topk", ctypes.c_uint32), ("groups", ctypes.c_uint32),
+                ("top_groups", ctypes.c_uint32), ("group_best", ctypes.c_uint32), ("renormalize", ctypes.c_uint32),
+                ("scale", ctypes.c_float)]
 
 
 _lib_handle = None
@@ -104,9 +121,17 @@ def lib() -> ctypes.CDLL:
         L.dfx_debug_inject.argtypes = [ctypes.c_uint32]
         L.dfx_encode_static.argtypes = [vp, ctypes.c_uint64, ctypes.POINTER(dfx_params), vp, ctypes.c_size_t,
                                         ctypes.POINTER(ctypes.c_size_t), vp]
+        u64, u32, sz = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_size_t
+        rp = ctypes.POINTER(dfx_route_params)
+        L.dfx_route_workspace.argtypes = [u64, u32, rp, ctypes.POINTER(sz)]
+        L.dfx_route.argtypes = [vp, vp, u32, u64, u64, u32, vp, rp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dfx_quantize_fp8.argtypes = [vp, vp, u32, u64, u64, vp, u64, u64, u32, u32, vp, u64, vp, u64, vp]
+        L.dfx_gemm_fp8.argtypes = [vp, vp, u64, vp, u64, u64, vp, u64, vp, u64, u64, u64, u32, vp, vp, u32, u64, vp]
+        L.dfx_combine.argtypes = [vp, vp, u32, u64, u64, u64, vp, vp, u64, u32, vp, u32, u64, vp]
         for f in ("dfx_container_layout", "dfx_plan", "dfx_encode", "dfx_decode", "dfx_decode_range", "dfx_decode_host",
                   "dfx_decode_gemm", "dfx_decode_batch",
-                  "dfx_device_status", "dfx_free", "dfx_encode_static", "dfx_debug_inject"):
+                  "dfx_device_status", "dfx_free", "dfx_encode_static", "dfx_debug_inject", "dfx_route_workspace",
+                  "dfx_route", "dfx_quantize_fp8", "dfx_gemm_fp8", "dfx_combine"):
             getattr(L, f).restype = ctypes.c_int
         _lib_handle = L
     return _lib_handle
@@ -279,6 +304,46 @@ def dfx_encode_static(d_bf16, n: int, d_out, out_capacity: int, want_size: bool 
                                  ctypes.byref(size) if want_size else None, _stream(stream))
     _check(rc, "dfx_encode_static")
     return size.value if want_size else None
+
+
+def dfx_route_workspace(tokens: int, experts: int, params: dfx_route_params) -> int:
+    size = ctypes.c_size_t()
+    _check(lib().dfx_route_workspace(tokens, experts, ctypes.byref(params), ctypes.byref(size)), "dfx_route_workspace")
+    return size.value
+
+
+def dfx_route(plan: Plan, d_logits, logits_type: int, ld_logits: int, tokens: int, experts: int, d_bias,
+              params: dfx_route_params, d_ids, d_weights, d_offsets=None, d_rows=None, d_slots=None, d_workspace=None,
+              workspace_bytes: int = 0, stream=None) -> None:
+    """Each token's best experts and their weights; with d_offsets, d_rows and d_slots also
+    the assignments sorted by expert."""
+    _check(lib().dfx_route(plan.handle, _ptr(d_logits), logits_type, ld_logits, tokens, experts, _ptr(d_bias),
+                           ctypes.byref(params), _ptr(d_ids), _ptr(d_weights), _ptr(d_offsets), _ptr(d_rows),
+                           _ptr(d_slots), _ptr(d_workspace), workspace_bytes, _stream(stream)), "dfx_route")
+
+
+def dfx_quantize_fp8(plan: Plan, d_x, x_type: int, ld_x: int, x_rows: int, d_index, rows: int, cols: int,
+                     block_rows: int, flags: int, d_q, ld_q: int, d_scales, ld_scales: int, stream=None) -> None:
+    """e4m3 values and e8m0 scales of 1x128 (block_rows 1) or 128x128 (128) blocks."""
+    _check(lib().dfx_quantize_fp8(plan.handle, _ptr(d_x), x_type, ld_x, x_rows, _ptr(d_index), rows, cols, block_rows,
+                                  flags, _ptr(d_q), ld_q, _ptr(d_scales), ld_scales, _stream(stream)),
+           "dfx_quantize_fp8")
+
+
+def dfx_gemm_fp8(plan: Plan, d_x, ld_x: int, d_x_scales, ld_x_scales: int, tokens: int, d_w, ld_w: int, d_w_scales,
+                 ld_w_scales: int, rows: int, cols: int, experts: int, d_offsets, d_y, y_type: int, ld_y: int,
+                 stream=None) -> None:
+    """Y = X W^T of dfx_quantize_fp8's operands, with one matrix or one per expert (d_offsets)."""
+    _check(lib().dfx_gemm_fp8(plan.handle, _ptr(d_x), ld_x, _ptr(d_x_scales), ld_x_scales, tokens, _ptr(d_w), ld_w,
+                              _ptr(d_w_scales), ld_w_scales, rows, cols, experts, _ptr(d_offsets), _ptr(d_y), y_type,
+                              ld_y, _stream(stream)), "dfx_gemm_fp8")
+
+
+def dfx_combine(plan: Plan, d_z, z_type: int, ld_z: int, z_rows: int, cols: int, d_slots, d_weights, tokens: int,
+                topk: int, d_y, y_type: int, ld_y: int, stream=None) -> None:
+    """y[t] = sum over k of weights[t, k] z[slots[t, k]]."""
+    _check(lib().dfx_combine(plan.handle, _ptr(d_z), z_type, ld_z, z_rows, cols, _ptr(d_slots), _ptr(d_weights), tokens,
+                             topk, _ptr(d_y), y_type, ld_y, _stream(stream)), "dfx_combine")
 
 
 # ---------------------------------------------------------------- tensor helpers

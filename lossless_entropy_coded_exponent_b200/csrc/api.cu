@@ -6,30 +6,14 @@
 
 #include "dfx.h"
 #include "dfx_common.cuh"
+#include "plan.cuh"
 
-struct dfx_plan_s {
-    uint64_t n;
-    uint32_t K, G, max_len;
-    uint32_t coder, table_log;  // exponent coder; tANS table log (coder 1)
-    uint32_t decode_flags;      // DFX_DECODE_*
-    dfx::Layout L;
-    uint64_t max_bytes;
-    uint64_t ws_bytes;
-    uint32_t* d_status;
-    int device;
-    int sms;  // streaming multiprocessors of the device
-    int decode_grid;
-    int resident_ctas;  // decode CTAs that fit on the device at once
-    // events ordering dfx_decode_host's copies before the decode of their slices,
-    // created on first use
-    static constexpr uint32_t kHostSlicesMax = 64;
-    cudaEvent_t slice_done[kHostSlicesMax];
-    // recorded on the decode stream when dfx_decode_host starts: its copies into the
-    // staging buffer wait for the decoding already queued there (an earlier call's
-    // slices may still be reading the buffer)
-    cudaEvent_t decode_idle;
-    bool events_made;
-};
+using dfx::aligned16;
+using dfx::check_device;
+
+namespace dfx {
+uint32_t g_inject = 0;
+}
 
 namespace {
 
@@ -69,18 +53,8 @@ uint64_t max_stream_bits(const Params& q, uint64_t n, uint64_t n_chunk) {
     return dfx::is_tans(q.coder) ? (uint64_t)q.R * (n + dfx::tans_states(q.coder) * n_chunk) : 8 * n;
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-uint32_t g_inject = 0;  // dfx_debug_inject
-
 // Host checks of one decode and its kernel arguments.
 int make_decode_args(const dfx_plan_s* plan, const void* d_comp, size_t comp_bytes, void* d_bf16, dfx::DecodeArgs* a);
-
-int check_device(const dfx_plan_s* plan) {
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return DFX_ERR_CUDA;
-    return dev == plan->device ? DFX_OK : DFX_ERR_ARG;
-}
 
 }  // namespace
 
@@ -89,8 +63,8 @@ extern "C" {
 uint32_t dfx_version(void) { return (1u << 16) | 0u; }
 
 int dfx_debug_inject(uint32_t flags) {
-    if (flags & ~(uint32_t)DFX_INJECT_SKIP_SLICE_COPY) return DFX_ERR_ARG;
-    g_inject = flags;
+    if (flags & ~(uint32_t)(DFX_INJECT_SKIP_SLICE_COPY | DFX_INJECT_SKIP_TILE_COPY)) return DFX_ERR_ARG;
+    dfx::g_inject = flags;
     return DFX_OK;
 }
 
@@ -441,7 +415,7 @@ int make_decode_args(const dfx_plan_s* plan, const void* d_comp, size_t comp_byt
     a->g_begin = 0;
     a->g_end = (uint32_t)plan->L.n_group;
     a->out_first = 0;
-    a->inject = g_inject;
+    a->inject = dfx::g_inject & DFX_INJECT_SKIP_SLICE_COPY;
     a->early = (plan->decode_flags & DFX_DECODE_EARLY_READ) ? 1u : 0u;
     return DFX_OK;
 }

@@ -48,6 +48,7 @@
 #include "decode_pipeline.cuh"
 #include "huffman_reader.cuh"
 #include "huffman_tables.cuh"
+#include "tcgen05.cuh"
 
 namespace dfx {
 namespace {
@@ -61,7 +62,6 @@ constexpr int kGemmTileRows = 128;    // MMA M (tile rows past the tile's own ar
 static_assert(kGemmMaxRows <= kGemmTileRows, "the rows of a tile fit the MMA's M = 128");
 constexpr int kGemmThreads = (kGemmDecodeWarps + 1) * 32;
 constexpr uint32_t kRoundsPerGroup = 32 / kGemmLanesPerRow;
-constexpr uint32_t kAtomBytes = 128;                           // one swizzle row: 64 BF16
 constexpr uint32_t kStageAtoms = 2;                            // K atoms (blocks of the round) per stage
 constexpr uint32_t kAAtomBytes = kGemmTileRows * kAtomBytes;    // 16 KiB: 128 rows x 64 K
 constexpr uint32_t kAStageBytes = kStageAtoms * kAAtomBytes;    // 32 KiB
@@ -70,73 +70,6 @@ constexpr uint32_t kTmemCols = 32;                             // FP32 accumulat
 constexpr uint32_t kSliceBytes = 416;                          // a row's stream slice for one round
 constexpr uint32_t kSliceWords = kSliceBytes / 4;
 static_assert(kSliceBytes % 16 == 0, "bulk copies move 16-byte units");
-
-// ---------------------------------------------------------------- tcgen05 helpers
-
-// Shared-memory matrix descriptor of a K-major tile with the 128-byte swizzle: 8-row
-// groups 1024 bytes apart (stride byte offset), leading byte offset 16 (unused by this
-// layout), descriptor version 1 (sm_100), layout type 2 (128-byte swizzle).  The tile
-// base is 1024-byte aligned, so the base-offset field stays 0.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-// Instruction descriptor of kind::f16: FP32 accumulator, BF16 A and B, both K-major,
-// N = n (multiple of 16), M = 128.
-__host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t n) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((128u >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-// arrives on `bar` once every tcgen05 operation this thread issued before has completed
-__device__ __forceinline__ void mma_commit(unsigned long long* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_addr(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void mbar_init_count(unsigned long long* bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_addr(bar)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_addr(bar)) : "memory");
-}
-// 16 FP32 accumulator columns of this warp's 32 tensor-memory lanes
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];\n"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-}
-// 16 bytes from global src to shared dst without a register stage; zeros when !valid
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(valid ? 16u : 0u)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-// waits until at most the newest committed group of this thread's copies is in flight
-__device__ __forceinline__ void cp_async_wait_prior() { asm volatile("cp.async.wait_group 1;\n" ::: "memory"); }
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-
-// Byte offset of (row r, 16-byte chunk c of K atom a) in a K-major 128-byte-swizzled tile
-// of `rows` rows: atoms one after another, 8-row groups 1024 bytes apart, row r of its
-// group at 128 (r mod 8), its chunk c at chunk c ^ (r mod 8).
-__device__ __forceinline__ uint32_t sw128_offset(uint32_t rows, uint32_t r, uint32_t a, uint32_t c) {
-    return a * rows * kAtomBytes + (r >> 3) * 1024u + (r & 7u) * kAtomBytes + ((c ^ (r & 7u)) << 4);
-}
 
 // ---------------------------------------------------------------- the kernel
 

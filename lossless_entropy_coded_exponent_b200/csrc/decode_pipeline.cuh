@@ -42,6 +42,7 @@
 
 #include "bulk.cuh"
 #include "dfx_common.cuh"
+#include "launch.cuh"
 
 namespace dfx {
 namespace {
@@ -428,7 +429,6 @@ __device__ void decode_tail_group(const DecodeArgs& a, const typename C::Tables&
 // preceding kernel does not write the container (DFX_DECODE_EARLY_READ), only before its
 // first output write: its header checks, table build and first copies then overlap the
 // preceding kernel's last groups.
-__device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void enter_dependent(const DecodeArgs& a) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (!a.early) wait_prior_grid();
@@ -511,34 +511,6 @@ int blocks_per_sm() {
                                                       dyn_smem_bytes<C, K>()) != cudaSuccess)
         return 1;
     return b > 0 ? b : 1;
-}
-
-// The dynamic shared-memory limit of a kernel is raised once per device (needed above
-// 48 KiB).
-template <class F>
-cudaError_t allow_smem(F* kernel, size_t bytes, bool* done) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
-    return e;
-}
-
-// Launch with programmatic stream serialisation (the kernel starts with enter_dependent).
-template <class Kern, class Arg>
-cudaError_t launch_programmatic(Kern* kernel, int grid, int threads, size_t smem, cudaStream_t s, const Arg& arg) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, arg);
 }
 
 template <class C, int K>

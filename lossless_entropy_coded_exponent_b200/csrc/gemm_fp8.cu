@@ -1,0 +1,421 @@
+// gemm_fp8.cu -- Y = X W^T with X and W in e4m3 and a power-of-two scale for each 128 values
+// of a token's row and each 128 x 128 block of W; one matrix, or one per expert with the
+// expert's own run of X's rows.
+//
+// The scales go into the tensor cores with the values: tcgen05.mma kind::mxf8f6f4 multiplies
+// by e8m0 scale bytes held in tensor memory, one per row and 32 values of K, so the four MMAs
+// of a 128-value block name the same byte and the whole sum over K stays in one FP32
+// accumulator.
+//
+// W's rows are the MMA's M (a tile is 128 rows: one row of scale blocks), tokens its N: 16 to
+// kCap columns, chosen per tile, so one token and a thousand run through the same code and no
+// token is padded to 128 rows.  A tile (unit) is one expert's 128 rows by up to kCap of its
+// tokens.  A persistent CTA per SM takes units in turn.  Warps:
+//   0     brings the tiles in by TMA (128-byte swizzle), kStages deep;
+//   1     issues the MMAs and copies each group of four blocks' scale bytes from shared to
+//         tensor memory; owns the tensor memory;
+//   2     lays out the scale bytes in shared memory: byte j of word (32 i + l) of a 512-byte
+//         tile is the scale of row 32 i + l and block 4 g + j (row l's four words are
+//         neighbours), which tcgen05.cp spreads over the lanes;
+//   4-7   read the accumulator (lane = row of W) and write Y, while the next unit's MMAs run
+//         into the other accumulator.
+// Every wait is bounded: one that runs out sets DFX_STATUS_TIMEOUT, the CTA's warps leave their
+// loops, and the copies and MMAs in flight are waited for before the tensor memory is freed.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "dfx_common.cuh"
+#include "experts.cuh"
+#include "launch.cuh"
+#include "tcgen05.cuh"
+#include "vec.cuh"
+
+namespace dfx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr uint32_t kTileRows = 128;                       // rows of W per tile: the MMA's M
+constexpr uint32_t kTileK = 128;                          // values of K per stage: one scale block
+constexpr uint32_t kABytes = kTileRows * kTileK;          // 16 KiB
+constexpr uint32_t kScaleTile = 512;                      // scale bytes of 128 rows x 4 blocks
+constexpr uint32_t kGroup = 4;                            // blocks of K per scale tile
+constexpr uint32_t kTmemColumns = 512;                    // one CTA per SM: all of it
+
+// kCap: most tokens of a tile; kBox: tokens of one TMA copy
+template <uint32_t CAP>
+struct Shape {
+    static constexpr uint32_t kCap = CAP;
+    static constexpr uint32_t kBox = CAP == 240 ? 80 : 32;
+    static constexpr uint32_t kStages = CAP == 32 ? 9 : CAP == 128 ? 6 : 4;
+    static constexpr uint32_t kBBytes = CAP * kTileK;
+    static constexpr uint32_t kStageBytes = kABytes + kBBytes;
+    static constexpr uint32_t kSlots = CAP == 240 ? 2 : 4;             // scale groups in flight
+    static constexpr uint32_t kBTiles = (CAP + 127) / 128;             // scale tiles of the tokens
+    static constexpr uint32_t kSlotBytes = (1 + kBTiles) * kScaleTile;
+    static constexpr uint32_t kSlotColumns = 4 * (1 + kBTiles);        // tensor memory of a slot
+    static constexpr uint32_t kScaleColumn = 2 * CAP;                  // behind the two accumulators
+    static_assert(CAP % 16 == 0 && CAP % kBox == 0 && kBox % 8 == 0, "whole MMA columns and swizzle groups");
+    static_assert(kStageBytes % 1024 == 0, "the swizzle pattern starts every 1024 bytes");
+    static_assert(kScaleColumn + kSlots * kSlotColumns <= kTmemColumns, "tensor memory");
+    static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kSlots * kSlotBytes;
+    static_assert(kSmem + 8192 <= 227 * 1024, "shared memory");
+};
+
+// Instruction descriptor of kind::mxf8f6f4: FP32 accumulator, e4m3 A and B, K-major, e8m0
+// scales of which byte `sf` of each word is taken, N = n (a multiple of 16), M = 128.
+__device__ __forceinline__ uint32_t idesc_e4m3(uint32_t n, uint32_t sf) {
+    return (sf << 4) | ((n >> 3) << 17) | (1u << 23) | (1u << 27) | (sf << 29);
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+// 512 bytes of shared memory, 32 rows of 16 bytes, to four columns of 32 tensor-memory lanes,
+// repeated in each quarter of the lanes; MMAs this thread issues later see them
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+    // no swizzle, 8-row groups 128 bytes apart, descriptor version 1
+    const uint64_t desc = (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
+}
+// a box of `map` at (x, y) to shared memory; x is a multiple of 128 bytes
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t x, uint32_t y,
+                                         unsigned long long* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void expect_bytes(unsigned long long* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+
+struct KernelArgs {
+    GemmFp8Args g;
+    uint32_t row_tiles, blocks;  // 128-row tiles of a matrix, 128-value blocks of K
+};
+
+// One unit of work
+struct Unit {
+    uint32_t expert, row_tile;
+    uint32_t first, n;   // its tokens
+    uint32_t columns;    // n rounded up to the MMA's 16
+};
+
+// Units in order: experts, then runs of tokens, then row tiles.  start[e]: units of the experts
+// before e; every warp that walks the units keeps its own expert.
+template <class S>
+struct Walk {
+    const KernelArgs& a;
+    const uint32_t* start;
+    const uint32_t* edge;  // first row of X of each expert, and one past the last
+    uint32_t e = 0;
+    __device__ __forceinline__ Walk(const KernelArgs& a_, const uint32_t* s, const uint32_t* x) : a(a_), start(s), edge(x) {}
+    __device__ __forceinline__ Unit at(uint32_t u) {
+        while (u >= start[e + 1]) e++;
+        const uint32_t tiles = (start[e + 1] - start[e]) / a.row_tiles, tokens = edge[2 * e + 1] - edge[2 * e];
+        const uint32_t local = u - start[e], run = local / a.row_tiles;
+        // the expert's tokens in `tiles` runs of nearly equal length
+        const uint32_t size = ((tokens + tiles - 1) / tiles + 15) & ~15u;
+        Unit w;
+        w.expert = e;
+        w.row_tile = local - run * a.row_tiles;
+        w.first = edge[2 * e] + min(tokens, run * size);
+        w.n = min(size, tokens - min(tokens, run * size));
+        w.columns = max(16u, (w.n + 15) & ~15u);
+        return w;
+    }
+};
+
+template <class S>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_gemm_fp8(const __grid_constant__ KernelArgs a, const __grid_constant__ CUtensorMap map_x,
+               const __grid_constant__ CUtensorMap map_w) {
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    __shared__ __align__(8) unsigned long long bar_full[S::kStages], bar_free[S::kStages], bar_scale[S::kSlots],
+        bar_scale_free[S::kSlots], bar_acc[2], bar_acc_free[2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile uint32_t stop;  // a wait ran out: every warp leaves its loop
+    extern __shared__ __align__(16) uint8_t dyn_smem[];
+    // behind the tiles: the experts' rows and first units
+    const uint32_t dyn0 = smem_addr(dyn_smem), pad = (1024u - (dyn0 & 1023u)) & 1023u;
+    const uint32_t tiles = dyn0 + pad, scales = tiles + S::kStages * S::kStageBytes;
+    uint8_t* scales_ptr = dyn_smem + pad + S::kStages * S::kStageBytes;
+    uint32_t* edge = reinterpret_cast<uint32_t*>(dyn_smem + S::kSmem);  // 2 per expert
+    uint32_t* start = edge + 2 * a.g.experts;                           // experts + 1
+
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(&tmem_slot)),
+                     "r"(kTmemColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    } else if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < S::kStages; i++) mbar_init_count(&bar_full[i], 1), mbar_init_count(&bar_free[i], 1);
+        for (uint32_t i = 0; i < S::kSlots; i++) mbar_init_count(&bar_scale[i], 1), mbar_init_count(&bar_scale_free[i], 1);
+        for (uint32_t i = 0; i < 2; i++) mbar_init_count(&bar_acc[i], 1), mbar_init_count(&bar_acc_free[i], 4);
+        fence_mbar_init();
+        stop = 0;
+    }
+    wait_prior_grid();
+    uint32_t err = 0;
+    // the experts' rows, clamped to X, and their units
+    for (uint32_t e = threadIdx.x; e < a.g.experts; e += kThreads) {
+        uint32_t lo = 0, hi = a.g.tokens;
+        if (a.g.offsets) {
+            const int32_t o0 = *(a.g.offsets + e), o1 = *(a.g.offsets + e + 1);
+            lo = (uint32_t)min(max(o0, 0), (int32_t)a.g.tokens);
+            hi = (uint32_t)min(max(o1, (int32_t)lo), (int32_t)a.g.tokens);
+            if ((int32_t)lo != o0 || (int32_t)hi != o1) err |= DFX_STATUS_INDEX;
+        }
+        edge[2 * e] = lo;
+        edge[2 * e + 1] = hi;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+        uint32_t carry = 0;
+        for (uint32_t e0 = 0; e0 < a.g.experts; e0 += 32) {
+            const uint32_t e = e0 + lane;
+            const uint32_t n = e < a.g.experts ? edge[2 * e + 1] - edge[2 * e] : 0;
+            const uint32_t v = (n + S::kCap - 1) / S::kCap * a.row_tiles;
+            uint32_t incl = v;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t y = __shfl_up_sync(kFull, incl, d);
+                if (lane >= (uint32_t)d) incl += y;
+            }
+            if (e < a.g.experts) start[e] = carry + incl - v;
+            carry += __shfl_sync(kFull, incl, 31);
+        }
+        if (lane == 0) start[a.g.experts] = carry;
+    }
+    __syncthreads();
+    const uint32_t tmem = tmem_slot, units = start[a.g.experts];
+    auto wait = [&](unsigned long long* bar, uint32_t parity) {
+        if (mbar_wait(bar, parity)) return stop == 0;
+        err |= DFX_STATUS_TIMEOUT;
+        stop = 1;
+        return false;
+    };
+    // the same for a whole warp, whose lanes go on or leave together
+    auto wait_warp = [&](unsigned long long* bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)) != 0; };
+    Walk<S> walk(a, start, edge);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ tiles
+        if (lane == 0) {
+            uint32_t st = 0, ph = 0, issued = 0;
+            bool skip = a.g.inject != 0;  // test hook: the first stage's copies are left out
+            bool ok = true;
+            for (uint32_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                const Unit w = walk.at(u);
+                const uint32_t boxes = (w.columns + S::kBox - 1) / S::kBox;
+                const uint32_t wy = w.expert * a.g.rows + w.row_tile * kTileRows;
+                for (uint32_t kb = 0; kb < a.blocks; kb++) {
+                    if (issued >= S::kStages && !(ok = wait(&bar_free[st], ph ^ 1u))) break;
+                    const uint32_t sA = tiles + st * S::kStageBytes, sB = sA + kABytes;
+                    if (!skip) {
+                        expect_bytes(&bar_full[st], kABytes + boxes * S::kBox * kTileK);
+                        tma_load(sA, &map_w, kb * kTileK, wy, &bar_full[st]);
+                        for (uint32_t b = 0; b < boxes; b++)
+                            tma_load(sB + b * S::kBox * kTileK, &map_x, kb * kTileK, w.first + b * S::kBox, &bar_full[st]);
+                    } else {
+                        ok = false;
+                        break;
+                    }
+                    issued++;
+                    if (++st == S::kStages) st = 0, ph ^= 1u;
+                }
+            }
+            if (!ok) {
+                // the last copies of every stage land before the CTA ends
+                for (uint32_t i = 0; i < S::kStages && i < issued; i++) {
+                    const uint32_t last = (issued - 1 - i);
+                    mbar_wait(&bar_full[last % S::kStages], (last / S::kStages) & 1u);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        if (lane == 0) {
+            uint32_t st = 0, ph = 0, slot = 0, slot_ph = 0, acc = 0, acc_ph = 0, unit = 0;
+            bool ok = true;
+            for (uint32_t u = blockIdx.x; ok && u < units; u += gridDim.x, unit++) {
+                const Unit w = walk.at(u);
+                const uint32_t d = tmem + acc * S::kCap;
+                if (unit >= 2 && !(ok = wait(&bar_acc_free[acc], acc_ph ^ 1u))) break;
+                tc_fence_after();
+                for (uint32_t kb = 0; kb < a.blocks; kb++) {
+                    const uint32_t sf = tmem + S::kScaleColumn + slot * S::kSlotColumns;
+                    if (kb % kGroup == 0) {
+                        if (!(ok = wait(&bar_scale[slot], slot_ph))) break;
+                        tc_fence_after();
+                        const uint32_t s = scales + slot * S::kSlotBytes;
+#pragma unroll
+                        for (uint32_t i = 0; i < 1 + S::kBTiles; i++) copy_scales(sf + 4 * i, s + i * kScaleTile);
+                    }
+                    if (!(ok = wait(&bar_full[st], ph))) break;
+                    tc_fence_after();
+                    const uint32_t sA = tiles + st * S::kStageBytes, sB = sA + kABytes;
+                    const uint32_t idesc = idesc_e4m3(w.columns, kb % kGroup);
+#pragma unroll
+                    for (uint32_t k = 0; k < kTileK / 32; k++)
+                        mma_e4m3(d, smem_desc_sw128(sA + 32 * k), smem_desc_sw128(sB + 32 * k), idesc, sf, sf + 4,
+                                 (kb | k) != 0);
+                    mma_commit(&bar_free[st]);
+                    if (++st == S::kStages) st = 0, ph ^= 1u;
+                    if (kb % kGroup == kGroup - 1 || kb + 1 == a.blocks) {
+                        mma_commit(&bar_scale_free[slot]);
+                        if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                mma_commit(&bar_acc[acc]);
+                if (++acc == 2) acc = 0, acc_ph ^= 1u;
+            }
+            if (!ok) {
+                // what was issued completes before the tensor memory is freed
+                mma_commit(&bar_acc[acc]);
+                mbar_wait(&bar_acc[acc], acc_ph);
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ scales
+        uint32_t slot = 0, slot_ph = 0, issued = 0;
+        bool ok = true;
+        for (uint32_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            const Unit w = walk.at(u);
+            const uint8_t* sw = a.g.sw + ((uint64_t)w.expert * a.row_tiles + w.row_tile) * a.g.ld_sw;
+            for (uint32_t kb = 0; kb < a.blocks; kb += kGroup) {
+                // four blocks' bytes are one aligned word of a row of scales
+                const uint32_t aw = *reinterpret_cast<const uint32_t*>(sw + kb);
+                uint32_t bw[4 * S::kBTiles];
+#pragma unroll
+                for (uint32_t i = 0; i < 4 * S::kBTiles; i++) {
+                    const uint32_t r = 32 * i + lane;
+                    bw[i] = r < w.n ? *reinterpret_cast<const uint32_t*>(a.g.sx + (uint64_t)(w.first + r) * a.g.ld_sx + kb)
+                                    : 0u;
+                }
+                if (issued >= S::kSlots && !(ok = wait_warp(&bar_scale_free[slot], slot_ph ^ 1u))) break;
+                uint4* dst = reinterpret_cast<uint4*>(scales_ptr + slot * S::kSlotBytes);
+                dst[lane] = make_uint4(aw, aw, aw, aw);
+#pragma unroll
+                for (uint32_t i = 0; i < S::kBTiles; i++)
+                    dst[32 * (i + 1) + lane] = make_uint4(bw[4 * i], bw[4 * i + 1], bw[4 * i + 2], bw[4 * i + 3]);
+                fence_proxy_async();  // read by tcgen05.cp
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_scale[slot]);
+                issued++;
+                if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ epilogue
+        const uint32_t quarter = warp - 4;  // tensor-memory lanes 32 quarter .. + 31
+        uint32_t acc = 0, acc_ph = 0;
+        for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+            const Unit w = walk.at(u);
+            if (!wait_warp(&bar_acc[acc], acc_ph)) break;
+            tc_fence_after();
+            const uint32_t row = w.row_tile * kTileRows + 32 * quarter + lane;
+            const uint32_t taddr = tmem + acc * S::kCap + ((32 * quarter) << 16);
+            for (uint32_t c = 0; c < w.columns; c += 16) {
+                uint32_t v[16];
+                tmem_ld16(taddr + c, v);
+                if (row < a.g.rows) {
+                    const uint64_t o = (uint64_t)(w.first + c) * a.g.ld_y + row;
+#pragma unroll
+                    for (uint32_t j = 0; j < 16; j++) {
+                        if (c + j >= w.n) break;
+                        if (a.g.y_f32) ((float*)a.g.y)[o + j * a.g.ld_y] = __uint_as_float(v[j]);
+                        else ((__nv_bfloat16*)a.g.y)[o + j * a.g.ld_y] = __float2bfloat16_rn(__uint_as_float(v[j]));
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_acc_free[acc]);
+            if (++acc == 2) acc = 0, acc_ph ^= 1u;
+        }
+    }
+    __syncwarp();
+    if (err) atomicOr(a.g.status, err);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kTmemColumns) : "memory");
+    }
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// the driver's call, looked up once (the library links no driver library)
+EncodeTiled encode_tiled() {
+    static EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return (EncodeTiled)p;
+    }();
+    return fn;
+}
+
+// rows x cols bytes, `ld` apart, in boxes of box_rows x 128; what lies past cols or rows reads 0
+bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+    const EncodeTiled fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld};
+    const cuuint32_t box[2] = {kTileK, box_rows}, steps[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, steps,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <uint32_t CAP>
+cudaError_t launch(const GemmFp8Args& g, int sms, cudaStream_t s) {
+    using S = Shape<CAP>;
+    KernelArgs a;
+    memset(&a, 0, sizeof(a));
+    a.g = g;
+    a.row_tiles = (g.rows + kTileRows - 1) / kTileRows;
+    a.blocks = (g.cols + kTileK - 1) / kTileK;
+    CUtensorMap mx, mw;
+    if (!make_map(&mx, g.x, g.tokens, g.cols, g.ld_x, S::kBox) ||
+        !make_map(&mw, g.w, (uint64_t)g.experts * g.rows, g.cols, g.ld_w, kTileRows))
+        return cudaErrorInvalidValue;
+    static bool attr_set[64] = {};
+    const size_t most = S::kSmem + (3 * kMaxGemmExperts + 1) * sizeof(uint32_t);
+    static_assert(S::kSmem + (3 * kMaxGemmExperts + 1) * sizeof(uint32_t) + 1024 <= 227 * 1024, "shared memory");
+    const cudaError_t e = allow_smem(k_gemm_fp8<S>, most, attr_set);
+    if (e != cudaSuccess) return e;
+    // at most this many units: an expert's last run of tokens may be short
+    const uint64_t runs = g.offsets ? (uint64_t)g.tokens / CAP + (g.experts < g.tokens ? g.experts : g.tokens)
+                                    : ((uint64_t)g.tokens + CAP - 1) / CAP;
+    const uint64_t units = runs * a.row_tiles;
+    const int grid = (int)(units < (uint64_t)sms ? units : (uint64_t)sms);
+    return launch_programmatic(k_gemm_fp8<S>, grid, kThreads, S::kSmem + (3 * g.experts + 1) * sizeof(uint32_t), s, a, mx, mw);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp8(const GemmFp8Args& g, int sms, cudaStream_t s) {
+    // the smallest tile that holds an expert's usual tokens: its copies of X are short and its
+    // pipeline is deep
+    const uint64_t mean = (g.tokens + g.experts - 1) / g.experts;
+    return mean <= 32 ? launch<32>(g, sms, s) : mean <= 128 ? launch<128>(g, sms, s) : launch<240>(g, sms, s);
+}
+
+}  // namespace dfx
