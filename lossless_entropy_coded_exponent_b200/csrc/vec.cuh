@@ -33,6 +33,14 @@ struct Eight<__nv_bfloat16> {
         unpack_bf16(p.z, v[4], v[5]);
         unpack_bf16(p.w, v[6], v[7]);
     }
+    // n (0 .. 8) values one by one, the others zero
+    __device__ __forceinline__ void load_some(const __nv_bfloat16* s, uint32_t n) {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(s);
+        uint32_t w[8];
+#pragma unroll
+        for (uint32_t i = 0; i < 8; i++) w[i] = i < n ? h[i] : 0u;
+        p = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
 };
 template <>
 struct Eight<float> {
@@ -45,6 +53,13 @@ struct Eight<float> {
     __device__ __forceinline__ void get(float (&v)[8]) const {
         v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
         v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
+    }
+    __device__ __forceinline__ void load_some(const float* s, uint32_t n) {
+        float v[8];
+#pragma unroll
+        for (uint32_t i = 0; i < 8; i++) v[i] = i < n ? s[i] : 0.0f;
+        p = make_float4(v[0], v[1], v[2], v[3]);
+        q = make_float4(v[4], v[5], v[6], v[7]);
     }
 };
 
