@@ -33,22 +33,40 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
 // 128 ns between them (__nanosleep(64) lasts at most twice its argument); a wait that
 // never completes gives up after ~0.1 ms + ~0.35 s and the caller reports
 // DFX_STATUS_TIMEOUT.
+// CLUSTER: what other CTAs of the cluster wrote before they arrived is visible afterwards.
 constexpr uint32_t kWaitPolls = 1u << 21;
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(unsigned long long* bar, uint32_t parity) {
     const uint32_t addr = smem_addr(bar);
     uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    if (done) return true;
-    for (uint32_t i = 0; i < kWaitPolls; i++) {
+    if constexpr (CLUSTER)
         asm volatile(
-            "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 100000;\n selp.u32 %0, "
+            "1, 0, p;\n}\n"
             : "=r"(done)
             : "r"(addr), "r"(parity)
             : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(addr), "r"(parity)
+            : "memory");
+    if (done) return true;
+    for (uint32_t i = 0; i < kWaitPolls; i++) {
+        if constexpr (CLUSTER)
+            asm volatile(
+                "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, "
+                "0, p;\n}\n"
+                : "=r"(done)
+                : "r"(addr), "r"(parity)
+                : "memory");
+        else
+            asm volatile(
+                "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                : "=r"(done)
+                : "r"(addr), "r"(parity)
+                : "memory");
         if (done) return true;
         __nanosleep(64);
     }

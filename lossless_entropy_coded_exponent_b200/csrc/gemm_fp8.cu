@@ -42,22 +42,26 @@ constexpr uint32_t kTileK = 128;                          // values of K per sta
 constexpr uint32_t kABytes = kTileRows * kTileK;          // 16 KiB
 constexpr uint32_t kScaleTile = 512;                      // scale bytes of 128 rows x 4 blocks
 constexpr uint32_t kGroup = 4;                            // blocks of K per scale tile
+constexpr uint32_t kChunkGroups = 4;                      // scale tiles whose words are loaded at once
 constexpr uint32_t kTmemColumns = 512;                    // one CTA per SM: all of it
 
-// kCap: most tokens of a tile; kBox: tokens of one TMA copy
-template <uint32_t CAP>
+// kCap: most tokens of a tile; kBox: tokens of one TMA copy; kPair: the two CTAs of a cluster
+// multiply 256 rows of W together, each holding its own 128 rows and half of the tokens
+template <uint32_t CAP, bool PAIR>
 struct Shape {
     static constexpr uint32_t kCap = CAP;
-    static constexpr uint32_t kBox = CAP == 240 ? 80 : 32;
-    static constexpr uint32_t kStages = CAP == 32 ? 9 : CAP == 128 ? 6 : 4;
-    static constexpr uint32_t kBBytes = CAP * kTileK;
-    static constexpr uint32_t kStageBytes = kABytes + kBBytes;
-    static constexpr uint32_t kSlots = CAP == 240 ? 2 : 4;             // scale groups in flight
+    static constexpr bool kPair = PAIR;
+    static constexpr uint32_t kCtas = PAIR ? 2 : 1;
+    static constexpr uint32_t kHeld = CAP / kCtas;                     // tokens in one CTA's memory
+    static constexpr uint32_t kBox = PAIR ? 40 : 32;
+    static constexpr uint32_t kStages = CAP == 32 ? 9 : 6;
+    static constexpr uint32_t kStageBytes = kABytes + kHeld * kTileK;
+    static constexpr uint32_t kSlots = PAIR ? 2 : 4;                   // scale groups in flight
     static constexpr uint32_t kBTiles = (CAP + 127) / 128;             // scale tiles of the tokens
     static constexpr uint32_t kSlotBytes = (1 + kBTiles) * kScaleTile;
     static constexpr uint32_t kSlotColumns = 4 * (1 + kBTiles);        // tensor memory of a slot
     static constexpr uint32_t kScaleColumn = 2 * CAP;                  // behind the two accumulators
-    static_assert(CAP % 16 == 0 && CAP % kBox == 0 && kBox % 8 == 0, "whole MMA columns and swizzle groups");
+    static_assert(CAP % 16 == 0 && kHeld % kBox == 0 && kBox % 8 == 0, "whole MMA columns and swizzle groups");
     static_assert(kStageBytes % 1024 == 0, "the swizzle pattern starts every 1024 bytes");
     static_assert(kScaleColumn + kSlots * kSlotColumns <= kTmemColumns, "tensor memory");
     static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kSlots * kSlotBytes;
@@ -65,71 +69,166 @@ struct Shape {
 };
 
 // Instruction descriptor of kind::mxf8f6f4: FP32 accumulator, e4m3 A and B, K-major, e8m0
-// scales of which byte `sf` of each word is taken, N = n (a multiple of 16), M = 128.
-__device__ __forceinline__ uint32_t idesc_e4m3(uint32_t n, uint32_t sf) {
-    return (sf << 4) | ((n >> 3) << 17) | (1u << 23) | (1u << 27) | (sf << 29);
+// scales, N = n (a multiple of 16), M = 128 per CTA; | sf_id(j): byte j of each scale word.
+__device__ __forceinline__ uint32_t idesc_e4m3(uint32_t n, uint32_t ctas) {
+    return ((n >> 3) << 17) | (1u << 23) | (ctas << 27);
 }
+__device__ __forceinline__ constexpr uint32_t sf_id(uint32_t j) { return (j << 4) | (j << 29); }
+
+template <bool PAIR>
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                          uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+            : "memory");
 }
 // 512 bytes of shared memory, 32 rows of 16 bytes, to four columns of 32 tensor-memory lanes,
-// repeated in each quarter of the lanes; MMAs this thread issues later see them
+// repeated in each quarter of the lanes (of both CTAs of a pair, each from its own shared
+// memory); MMAs this thread issues later see them
+template <bool PAIR>
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
     // no swizzle, 8-row groups 128 bytes apart, descriptor version 1
     const uint64_t desc = (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
+    if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
 }
-// a box of `map` at (x, y) to shared memory; x is a multiple of 128 bytes
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t x, uint32_t y,
-                                         unsigned long long* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
-        : "memory");
+// arrives on `bar` (of both CTAs of a pair) when what this thread issued has completed
+template <bool PAIR>
+__device__ __forceinline__ void commit(unsigned long long* bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+                smem_addr(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    else mma_commit(bar);
+}
+// a box of `map` at (x, y) to this CTA's shared memory; x is a multiple of 128.  The bytes
+// count on `bar`, of a pair the first CTA's.
+template <bool PAIR>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t x, uint32_t y, uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+            "%3}], [%4];\n" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+                dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
 }
 __device__ __forceinline__ void expect_bytes(unsigned long long* bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+// the address of `bar` in the first CTA of a pair
+template <bool PAIR>
+__device__ __forceinline__ uint32_t first_cta(unsigned long long* bar) {
+    uint32_t a = smem_addr(bar);
+    if constexpr (PAIR) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(a) : "r"(a));
+    return a;
+}
+template <bool PAIR>
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    if constexpr (PAIR) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+    else asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void sync_ctas() {
+    if constexpr (PAIR)
+        asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    else __syncthreads();
+}
+// one lane of a warp that is together
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
 }
 
 struct KernelArgs {
     GemmFp8Args g;
     uint32_t row_tiles, blocks;  // 128-row tiles of a matrix, 128-value blocks of K
+    uint32_t row_units;          // tiles, or pairs of tiles, of a matrix
+    uint32_t wide_sx, wide_sw;   // rows of scales in 16-byte pieces
 };
 
 // One unit of work
 struct Unit {
-    uint32_t expert, row_tile;
+    uint32_t expert, row_unit;
     uint32_t first, n;   // its tokens
     uint32_t columns;    // n rounded up to the MMA's 16
 };
 
-// Units in order: experts, then runs of tokens, then row tiles.  start[e]: units of the experts
-// before e; every warp that walks the units keeps its own expert.
-template <class S>
+// Units in order: experts; then groups of kRunGroup runs of tokens; in a group the rows of W, so
+// that units near each other in time share W's rows and a few runs of X, and both come from L2.
+constexpr uint32_t kRunGroup = 8;
 struct Walk {
     const KernelArgs& a;
-    const uint32_t* start;
-    const uint32_t* edge;  // first row of X of each expert, and one past the last
+    const uint32_t* start;  // units of the experts before
+    const uint32_t* edge;   // first row of X of each expert, and one past the last
     uint32_t e = 0;
     __device__ __forceinline__ Walk(const KernelArgs& a_, const uint32_t* s, const uint32_t* x) : a(a_), start(s), edge(x) {}
     __device__ __forceinline__ Unit at(uint32_t u) {
         while (u >= start[e + 1]) e++;
-        const uint32_t tiles = (start[e + 1] - start[e]) / a.row_tiles, tokens = edge[2 * e + 1] - edge[2 * e];
-        const uint32_t local = u - start[e], run = local / a.row_tiles;
-        // the expert's tokens in `tiles` runs of nearly equal length
-        const uint32_t size = ((tokens + tiles - 1) / tiles + 15) & ~15u;
+        const uint32_t runs = (start[e + 1] - start[e]) / a.row_units, tokens = edge[2 * e + 1] - edge[2 * e];
+        const uint32_t local = u - start[e], group = local / (kRunGroup * a.row_units);
+        const uint32_t in_group = local - group * kRunGroup * a.row_units, wide = min(kRunGroup, runs - group * kRunGroup);
+        const uint32_t run = group * kRunGroup + in_group % wide;
+        // the expert's tokens in `runs` runs of nearly equal length
+        const uint32_t size = ((tokens + runs - 1) / runs + 15) & ~15u;
         Unit w;
         w.expert = e;
-        w.row_tile = local - run * a.row_tiles;
+        w.row_unit = in_group / wide;
         w.first = edge[2 * e] + min(tokens, run * size);
         w.n = min(size, tokens - min(tokens, run * size));
         w.columns = max(16u, (w.n + 15) & ~15u);
         return w;
+    }
+};
+
+// The scale words of four groups of blocks: W's row of scale blocks, and the rows of X that are
+// this lane's (lane, lane + 32, ...).
+template <class S>
+struct ScaleChunk {
+    static constexpr uint32_t kRows = (S::kCap + 31) / 32;
+    uint32_t w[kChunkGroups], x[4 * S::kBTiles][kChunkGroups];
+    // four words at p, of which those before `blocks` are there
+    static __device__ __forceinline__ void words(uint32_t (&v)[kChunkGroups], const uint8_t* p, bool whole, uint32_t blocks) {
+        if (whole) {
+            const uint4 q = *reinterpret_cast<const uint4*>(p);
+            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+        } else {
+#pragma unroll
+            for (uint32_t g = 0; g < kChunkGroups; g++)
+                v[g] = kGroup * g < blocks ? *reinterpret_cast<const uint32_t*>(p + kGroup * g) : 0u;
+        }
+    }
+    __device__ __forceinline__ void load(const KernelArgs& a, const Unit& u, uint32_t row_tile, uint32_t kb, uint32_t lane) {
+        // a pair's second tile may lie past W's last: its rows are not stored
+        const uint32_t t = min(row_tile, a.row_tiles - 1);
+        words(w, a.g.sw + ((uint64_t)u.expert * a.row_tiles + t) * a.g.ld_sw + kb, a.wide_sw, a.blocks - kb);
+#pragma unroll
+        for (uint32_t i = 0; i < 4 * S::kBTiles; i++) {
+            const uint32_t r = 32 * i + lane;
+            if (i < kRows && r < u.n) {
+                words(x[i], a.g.sx + (uint64_t)(u.first + r) * a.g.ld_sx + kb, a.wide_sx, a.blocks - kb);
+            } else {
+#pragma unroll
+                for (uint32_t g = 0; g < kChunkGroups; g++) x[i][g] = 0;
+            }
+        }
     }
 };
 
@@ -138,30 +237,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_gemm_fp8(const __grid_constant__ KernelArgs a, const __grid_constant__ CUtensorMap map_x,
                const __grid_constant__ CUtensorMap map_w) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    constexpr bool P = S::kPair;
     __shared__ __align__(8) unsigned long long bar_full[S::kStages], bar_free[S::kStages], bar_scale[S::kSlots],
         bar_scale_free[S::kSlots], bar_acc[2], bar_acc_free[2];
     __shared__ uint32_t tmem_slot;
-    __shared__ volatile uint32_t stop;  // a wait ran out: every warp leaves its loop
     extern __shared__ __align__(16) uint8_t dyn_smem[];
-    // behind the tiles: the experts' rows and first units
     const uint32_t dyn0 = smem_addr(dyn_smem), pad = (1024u - (dyn0 & 1023u)) & 1023u;
     const uint32_t tiles = dyn0 + pad, scales = tiles + S::kStages * S::kStageBytes;
     uint8_t* scales_ptr = dyn_smem + pad + S::kStages * S::kStageBytes;
+    // behind the tiles: the experts' rows and first units
     uint32_t* edge = reinterpret_cast<uint32_t*>(dyn_smem + S::kSmem);  // 2 per expert
     uint32_t* start = edge + 2 * a.g.experts;                           // experts + 1
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = P ? blockIdx.x % S::kCtas : 0, first = blockIdx.x / S::kCtas, step = gridDim.x / S::kCtas;
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(&tmem_slot)),
-                     "r"(kTmemColumns)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+        if constexpr (P) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(&tmem_slot)),
+                         "r"(kTmemColumns)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(&tmem_slot)),
+                         "r"(kTmemColumns)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+        }
     } else if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < S::kStages; i++) mbar_init_count(&bar_full[i], 1), mbar_init_count(&bar_free[i], 1);
-        for (uint32_t i = 0; i < S::kSlots; i++) mbar_init_count(&bar_scale[i], 1), mbar_init_count(&bar_scale_free[i], 1);
-        for (uint32_t i = 0; i < 2; i++) mbar_init_count(&bar_acc[i], 1), mbar_init_count(&bar_acc_free[i], 4);
+        for (uint32_t i = 0; i < S::kSlots; i++)
+            mbar_init_count(&bar_scale[i], S::kCtas), mbar_init_count(&bar_scale_free[i], 1);
+        for (uint32_t i = 0; i < 2; i++) mbar_init_count(&bar_acc[i], 1), mbar_init_count(&bar_acc_free[i], 4 * S::kCtas);
         fence_mbar_init();
-        stop = 0;
     }
     wait_prior_grid();
     uint32_t err = 0;
@@ -169,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t e = threadIdx.x; e < a.g.experts; e += kThreads) {
         uint32_t lo = 0, hi = a.g.tokens;
         if (a.g.offsets) {
-            const int32_t o0 = *(a.g.offsets + e), o1 = *(a.g.offsets + e + 1);
+            const int32_t o0 = a.g.offsets[e], o1 = a.g.offsets[e + 1];
             lo = (uint32_t)min(max(o0, 0), (int32_t)a.g.tokens);
             hi = (uint32_t)min(max(o1, (int32_t)lo), (int32_t)a.g.tokens);
             if ((int32_t)lo != o0 || (int32_t)hi != o1) err |= DFX_STATUS_INDEX;
@@ -177,15 +284,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         edge[2 * e] = lo;
         edge[2 * e + 1] = hi;
     }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
     if (warp == 0) {
         uint32_t carry = 0;
         for (uint32_t e0 = 0; e0 < a.g.experts; e0 += 32) {
             const uint32_t e = e0 + lane;
             const uint32_t n = e < a.g.experts ? edge[2 * e + 1] - edge[2 * e] : 0;
-            const uint32_t v = (n + S::kCap - 1) / S::kCap * a.row_tiles;
+            const uint32_t v = (n + S::kCap - 1) / S::kCap * a.row_units;
             uint32_t incl = v;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -196,123 +301,144 @@ __global__ void __launch_bounds__(kThreads, 1)
             carry += __shfl_sync(kFull, incl, 31);
         }
         if (lane == 0) start[a.g.experts] = carry;
+        __syncwarp();
     }
-    __syncthreads();
+    tc_fence_before();
+    sync_ctas<P>();
+    tc_fence_after();
     const uint32_t tmem = tmem_slot, units = start[a.g.experts];
+    // Every warp waits together and leaves together.  A wait that runs out ends its warp's loop;
+    // the other warps' waits then run out too.
     auto wait = [&](unsigned long long* bar, uint32_t parity) {
-        if (mbar_wait(bar, parity)) return stop == 0;
+        if (__all_sync(kFull, mbar_wait<P>(bar, parity))) return true;
         err |= DFX_STATUS_TIMEOUT;
-        stop = 1;
         return false;
     };
-    // the same for a whole warp, whose lanes go on or leave together
-    auto wait_warp = [&](unsigned long long* bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)) != 0; };
-    Walk<S> walk(a, start, edge);
+    Walk walk(a, start, edge);
 
     if (warp == 0) {
         // ------------------------------------------------------------ tiles
-        if (lane == 0) {
-            uint32_t st = 0, ph = 0, issued = 0;
-            bool skip = a.g.inject != 0;  // test hook: the first stage's copies are left out
-            bool ok = true;
-            for (uint32_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const Unit w = walk.at(u);
-                const uint32_t boxes = (w.columns + S::kBox - 1) / S::kBox;
-                const uint32_t wy = w.expert * a.g.rows + w.row_tile * kTileRows;
-                for (uint32_t kb = 0; kb < a.blocks; kb++) {
-                    if (issued >= S::kStages && !(ok = wait(&bar_free[st], ph ^ 1u))) break;
-                    const uint32_t sA = tiles + st * S::kStageBytes, sB = sA + kABytes;
-                    if (!skip) {
-                        expect_bytes(&bar_full[st], kABytes + boxes * S::kBox * kTileK);
-                        tma_load(sA, &map_w, kb * kTileK, wy, &bar_full[st]);
-                        for (uint32_t b = 0; b < boxes; b++)
-                            tma_load(sB + b * S::kBox * kTileK, &map_x, kb * kTileK, w.first + b * S::kBox, &bar_full[st]);
-                    } else {
-                        ok = false;
-                        break;
-                    }
-                    issued++;
-                    if (++st == S::kStages) st = 0, ph ^= 1u;
+        uint32_t st = 0, ph = 0, issued = 0;
+        bool ok = a.g.inject == 0;  // test hook: the copies are left out
+        for (uint32_t u = first; ok && u < units; u += step) {
+            const Unit w = walk.at(u);
+            // this CTA's tokens: all, or its half of the columns
+            const uint32_t held = w.columns / S::kCtas, token = w.first + rank * held;
+            const uint32_t boxes = (held + S::kBox - 1) / S::kBox;
+            const uint32_t row = w.expert * a.g.rows + (w.row_unit * S::kCtas + rank) * kTileRows;
+            for (uint32_t kb = 0; kb < a.blocks; kb++) {
+                if (issued >= S::kStages && !(ok = wait(&bar_free[st], ph ^ 1u))) break;
+                const uint32_t sA = tiles + st * S::kStageBytes, sB = sA + kABytes;
+                const uint32_t bar = first_cta<P>(&bar_full[st]);
+                if (elect_one()) {
+                    if (rank == 0) expect_bytes(&bar_full[st], S::kCtas * (kABytes + boxes * S::kBox * kTileK));
+                    tma_load<P>(sA, &map_w, kb * kTileK, row, bar);
+                    for (uint32_t b = 0; b < boxes; b++)
+                        tma_load<P>(sB + b * S::kBox * kTileK, &map_x, kb * kTileK, token + b * S::kBox, bar);
                 }
+                __syncwarp();
+                issued++;
+                if (++st == S::kStages) st = 0, ph ^= 1u;
             }
-            if (!ok) {
-                // the last copies of every stage land before the CTA ends
+        }
+        if (!ok && issued) {
+            // the copies in flight land before the CTA ends: those of each stage's last use, or,
+            // where their barrier is the other CTA's, within a thousand times their usual time
+            if constexpr (P) {
+                for (uint32_t i = 0; i < 1000; i++) __nanosleep(1000);
+            } else {
                 for (uint32_t i = 0; i < S::kStages && i < issued; i++) {
-                    const uint32_t last = (issued - 1 - i);
+                    const uint32_t last = issued - 1 - i;
                     mbar_wait(&bar_full[last % S::kStages], (last / S::kStages) & 1u);
                 }
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
-        if (lane == 0) {
+        if (rank == 0) {
             uint32_t st = 0, ph = 0, slot = 0, slot_ph = 0, acc = 0, acc_ph = 0, unit = 0;
             bool ok = true;
-            for (uint32_t u = blockIdx.x; ok && u < units; u += gridDim.x, unit++) {
+            const uint64_t descA = smem_desc_sw128(tiles), descB = smem_desc_sw128(tiles + kABytes);
+            for (uint32_t u = first; ok && u < units; u += step, unit++) {
                 const Unit w = walk.at(u);
-                const uint32_t d = tmem + acc * S::kCap;
-                if (unit >= 2 && !(ok = wait(&bar_acc_free[acc], acc_ph ^ 1u))) break;
-                tc_fence_after();
-                for (uint32_t kb = 0; kb < a.blocks; kb++) {
+                const uint32_t d = tmem + acc * S::kCap, idesc = idesc_e4m3(w.columns, S::kCtas);
+                if (unit >= 2) ok = wait(&bar_acc_free[acc], acc_ph ^ 1u);
+                for (uint32_t kb0 = 0; ok && kb0 < a.blocks; kb0 += kGroup) {
                     const uint32_t sf = tmem + S::kScaleColumn + slot * S::kSlotColumns;
-                    if (kb % kGroup == 0) {
-                        if (!(ok = wait(&bar_scale[slot], slot_ph))) break;
-                        tc_fence_after();
-                        const uint32_t s = scales + slot * S::kSlotBytes;
-#pragma unroll
-                        for (uint32_t i = 0; i < 1 + S::kBTiles; i++) copy_scales(sf + 4 * i, s + i * kScaleTile);
-                    }
-                    if (!(ok = wait(&bar_full[st], ph))) break;
+                    if (!(ok = wait(&bar_scale[slot], slot_ph))) break;
                     tc_fence_after();
-                    const uint32_t sA = tiles + st * S::kStageBytes, sB = sA + kABytes;
-                    const uint32_t idesc = idesc_e4m3(w.columns, kb % kGroup);
+                    if (elect_one()) {
 #pragma unroll
-                    for (uint32_t k = 0; k < kTileK / 32; k++)
-                        mma_e4m3(d, smem_desc_sw128(sA + 32 * k), smem_desc_sw128(sB + 32 * k), idesc, sf, sf + 4,
-                                 (kb | k) != 0);
-                    mma_commit(&bar_free[st]);
-                    if (++st == S::kStages) st = 0, ph ^= 1u;
-                    if (kb % kGroup == kGroup - 1 || kb + 1 == a.blocks) {
-                        mma_commit(&bar_scale_free[slot]);
-                        if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
+                        for (uint32_t i = 0; i < 1 + S::kBTiles; i++)
+                            copy_scales<P>(sf + 4 * i, scales + slot * S::kSlotBytes + i * kScaleTile);
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (uint32_t j = 0; j < kGroup; j++) {
+                        if (!ok || kb0 + j >= a.blocks) break;
+                        if (!(ok = wait(&bar_full[st], ph))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t at = (uint64_t)(st * (S::kStageBytes >> 4));
+#pragma unroll
+                            for (uint32_t k = 0; k < kTileK / 32; k++)
+                                mma_e4m3<P>(d, descA + at + 2 * k, descB + at + 2 * k, idesc | sf_id(j), sf, sf + 4,
+                                            (kb0 | j | k) != 0);
+                            commit<P>(&bar_free[st]);
+                        }
+                        __syncwarp();
+                        if (++st == S::kStages) st = 0, ph ^= 1u;
+                    }
+                    if (elect_one()) commit<P>(&bar_scale_free[slot]);
+                    __syncwarp();
+                    if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
                 }
-                if (!ok) break;
-                mma_commit(&bar_acc[acc]);
+                // the accumulator is ready; after a wait that ran out, what was issued completes
+                // before the tensor memory is freed
+                if (elect_one()) commit<P>(&bar_acc[acc]);
+                __syncwarp();
+                if (!ok) mbar_wait(&bar_acc[acc], acc_ph);
                 if (++acc == 2) acc = 0, acc_ph ^= 1u;
-            }
-            if (!ok) {
-                // what was issued completes before the tensor memory is freed
-                mma_commit(&bar_acc[acc]);
-                mbar_wait(&bar_acc[acc], acc_ph);
             }
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ scales
+        // chunks of four groups, one ahead of the group being laid out: a chunk's loads take a
+        // microsecond or more, a group's MMAs less
         uint32_t slot = 0, slot_ph = 0, issued = 0;
+        ScaleChunk<S> now, next;
+        uint32_t u = first, kb = 0;
+        Unit w;
+        if (u < units) {
+            w = walk.at(u);
+            next.load(a, w, w.row_unit * S::kCtas + rank, 0, lane);
+        }
         bool ok = true;
-        for (uint32_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-            const Unit w = walk.at(u);
-            const uint8_t* sw = a.g.sw + ((uint64_t)w.expert * a.row_tiles + w.row_tile) * a.g.ld_sw;
-            for (uint32_t kb = 0; kb < a.blocks; kb += kGroup) {
-                // four blocks' bytes are one aligned word of a row of scales
-                const uint32_t aw = *reinterpret_cast<const uint32_t*>(sw + kb);
-                uint32_t bw[4 * S::kBTiles];
+        while (ok && u < units) {
+            now = next;
+            const uint32_t groups = (min(a.blocks - kb, kGroup * kChunkGroups) + kGroup - 1) / kGroup;
+            kb += kGroup * kChunkGroups;
+            if (kb >= a.blocks) {
+                kb = 0;
+                u += step;
+                if (u < units) w = walk.at(u);
+            }
+            if (u < units) next.load(a, w, w.row_unit * S::kCtas + rank, kb, lane);
 #pragma unroll
-                for (uint32_t i = 0; i < 4 * S::kBTiles; i++) {
-                    const uint32_t r = 32 * i + lane;
-                    bw[i] = r < w.n ? *reinterpret_cast<const uint32_t*>(a.g.sx + (uint64_t)(w.first + r) * a.g.ld_sx + kb)
-                                    : 0u;
-                }
-                if (issued >= S::kSlots && !(ok = wait_warp(&bar_scale_free[slot], slot_ph ^ 1u))) break;
+            for (uint32_t g = 0; g < kChunkGroups; g++) {
+                if (g >= groups) break;
+                if (issued >= S::kSlots && !(ok = wait(&bar_scale_free[slot], slot_ph ^ 1u))) break;
                 uint4* dst = reinterpret_cast<uint4*>(scales_ptr + slot * S::kSlotBytes);
+                const uint32_t aw = now.w[g];
                 dst[lane] = make_uint4(aw, aw, aw, aw);
 #pragma unroll
                 for (uint32_t i = 0; i < S::kBTiles; i++)
-                    dst[32 * (i + 1) + lane] = make_uint4(bw[4 * i], bw[4 * i + 1], bw[4 * i + 2], bw[4 * i + 3]);
+                    dst[32 * (i + 1) + lane] =
+                        make_uint4(now.x[4 * i][g], now.x[4 * i + 1][g], now.x[4 * i + 2][g], now.x[4 * i + 3][g]);
                 fence_proxy_async();  // read by tcgen05.cp
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_scale[slot]);
+                const uint32_t bar = first_cta<P>(&bar_scale[slot]);
+                if (lane == 0) arrive<P>(bar);
                 issued++;
                 if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
             }
@@ -321,11 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ epilogue
         const uint32_t quarter = warp - 4;  // tensor-memory lanes 32 quarter .. + 31
         uint32_t acc = 0, acc_ph = 0;
-        for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+        for (uint32_t u = first; u < units; u += step) {
             const Unit w = walk.at(u);
-            if (!wait_warp(&bar_acc[acc], acc_ph)) break;
+            if (!wait(&bar_acc[acc], acc_ph)) break;
             tc_fence_after();
-            const uint32_t row = w.row_tile * kTileRows + 32 * quarter + lane;
+            const uint32_t row = (w.row_unit * S::kCtas + rank) * kTileRows + 32 * quarter + lane;
             const uint32_t taddr = tmem + acc * S::kCap + ((32 * quarter) << 16);
             for (uint32_t c = 0; c < w.columns; c += 16) {
                 uint32_t v[16];
@@ -339,20 +465,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else ((__nv_bfloat16*)a.g.y)[o + j * a.g.ld_y] = __float2bfloat16_rn(__uint_as_float(v[j]));
                     }
                 }
+                __syncwarp();
             }
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_acc_free[acc]);
+            const uint32_t bar = first_cta<P>(&bar_acc_free[acc]);
+            if (lane == 0) arrive<P>(bar);
             if (++acc == 2) acc = 0, acc_ph ^= 1u;
         }
     }
     __syncwarp();
     if (err) atomicOr(a.g.status, err);
     tc_fence_before();
-    __syncthreads();
+    sync_ctas<P>();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kTmemColumns) : "memory");
+        if constexpr (P)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kTmemColumns) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kTmemColumns) : "memory");
     }
 }
 
@@ -384,29 +514,33 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <uint32_t CAP>
+template <uint32_t CAP, bool PAIR>
 cudaError_t launch(const GemmFp8Args& g, int sms, cudaStream_t s) {
-    using S = Shape<CAP>;
+    using S = Shape<CAP, PAIR>;
     KernelArgs a;
     memset(&a, 0, sizeof(a));
     a.g = g;
     a.row_tiles = (g.rows + kTileRows - 1) / kTileRows;
+    a.row_units = (a.row_tiles + S::kCtas - 1) / S::kCtas;
     a.blocks = (g.cols + kTileK - 1) / kTileK;
+    a.wide_sx = g.ld_sx % 16 == 0;
+    a.wide_sw = g.ld_sw % 16 == 0;
     CUtensorMap mx, mw;
     if (!make_map(&mx, g.x, g.tokens, g.cols, g.ld_x, S::kBox) ||
         !make_map(&mw, g.w, (uint64_t)g.experts * g.rows, g.cols, g.ld_w, kTileRows))
         return cudaErrorInvalidValue;
     static bool attr_set[64] = {};
-    const size_t most = S::kSmem + (3 * kMaxGemmExperts + 1) * sizeof(uint32_t);
-    static_assert(S::kSmem + (3 * kMaxGemmExperts + 1) * sizeof(uint32_t) + 1024 <= 227 * 1024, "shared memory");
+    constexpr size_t most = S::kSmem + (3 * kMaxGemmExperts + 1) * sizeof(uint32_t);
+    static_assert(most + 1024 <= 227 * 1024, "shared memory");
     const cudaError_t e = allow_smem(k_gemm_fp8<S>, most, attr_set);
     if (e != cudaSuccess) return e;
     // at most this many units: an expert's last run of tokens may be short
     const uint64_t runs = g.offsets ? (uint64_t)g.tokens / CAP + (g.experts < g.tokens ? g.experts : g.tokens)
                                     : ((uint64_t)g.tokens + CAP - 1) / CAP;
-    const uint64_t units = runs * a.row_tiles;
-    const int grid = (int)(units < (uint64_t)sms ? units : (uint64_t)sms);
-    return launch_programmatic(k_gemm_fp8<S>, grid, kThreads, S::kSmem + (3 * g.experts + 1) * sizeof(uint32_t), s, a, mx, mw);
+    const uint64_t units = runs * a.row_units, room = (uint64_t)sms / S::kCtas;
+    const int grid = (int)((units < room ? units : room) * S::kCtas);
+    return launch_clusters(k_gemm_fp8<S>, grid, S::kCtas, kThreads, S::kSmem + (3 * g.experts + 1) * sizeof(uint32_t), s, a,
+                           mx, mw);
 }
 
 }  // namespace
@@ -415,7 +549,7 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& g, int sms, cudaStream_t s) {
     // the smallest tile that holds an expert's usual tokens: its copies of X are short and its
     // pipeline is deep
     const uint64_t mean = (g.tokens + g.experts - 1) / g.experts;
-    return mean <= 32 ? launch<32>(g, sms, s) : mean <= 128 ? launch<128>(g, sms, s) : launch<240>(g, sms, s);
+    return mean <= 32 ? launch<32, false>(g, sms, s) : mean <= 128 ? launch<128, false>(g, sms, s) : launch<240, true>(g, sms, s);
 }
 
 }  // namespace dfx

@@ -24,19 +24,27 @@ cudaError_t allow_smem(F* kernel, size_t bytes, bool* done) {
 
 // Launch with programmatic stream serialisation: the kernel may start while the work before it
 // in the stream finishes, and calls wait_prior_grid before it touches memory that work uses.
+// launch_clusters: in clusters of `ctas` CTAs.
 template <class Kern, class... Arg>
-cudaError_t launch_programmatic(Kern* kernel, int grid, int threads, size_t smem, cudaStream_t s, const Arg&... arg) {
+cudaError_t launch_clusters(Kern* kernel, int grid, unsigned ctas, int threads, size_t smem, cudaStream_t s,
+                            const Arg&... arg) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {ctas, 1, 1};
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, arg...);
+}
+template <class Kern, class... Arg>
+cudaError_t launch_programmatic(Kern* kernel, int grid, int threads, size_t smem, cudaStream_t s, const Arg&... arg) {
+    return launch_clusters(kernel, grid, 1, threads, smem, s, arg...);
 }
 
 }  // namespace
