@@ -35,6 +35,25 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
 // DFX_STATUS_TIMEOUT.
 // CLUSTER: what other CTAs of the cluster wrote before they arrived is visible afterwards.
 constexpr uint32_t kWaitPolls = 1u << 21;
+// one look at the phase, which may suspend the warp for a moment
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_poll(unsigned long long* bar, uint32_t parity) {
+    uint32_t done;
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, "
+            "p;\n}\n"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+    return done != 0;
+}
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(unsigned long long* bar, uint32_t parity) {
     const uint32_t addr = smem_addr(bar);

@@ -56,14 +56,15 @@ struct Shape {
     static constexpr uint32_t kBox = PAIR ? 40 : 32;
     static constexpr uint32_t kStages = CAP == 32 ? 9 : 6;
     static constexpr uint32_t kStageBytes = kABytes + kHeld * kTileK;
-    static constexpr uint32_t kSlots = PAIR ? 2 : 4;                   // scale groups in flight
+    static constexpr uint32_t kSlots = 4;                              // scale groups in shared memory
+    static constexpr uint32_t kCopies = 2;                             // and in tensor memory
     static constexpr uint32_t kBTiles = (CAP + 127) / 128;             // scale tiles of the tokens
     static constexpr uint32_t kSlotBytes = (1 + kBTiles) * kScaleTile;
     static constexpr uint32_t kSlotColumns = 4 * (1 + kBTiles);        // tensor memory of a slot
     static constexpr uint32_t kScaleColumn = 2 * CAP;                  // behind the two accumulators
     static_assert(CAP % 16 == 0 && kHeld % kBox == 0 && kBox % 8 == 0, "whole MMA columns and swizzle groups");
     static_assert(kStageBytes % 1024 == 0, "the swizzle pattern starts every 1024 bytes");
-    static_assert(kScaleColumn + kSlots * kSlotColumns <= kTmemColumns, "tensor memory");
+    static_assert(kScaleColumn + kCopies * kSlotColumns <= kTmemColumns, "tensor memory");
     static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kSlots * kSlotBytes;
     static_assert(kSmem + 8192 <= 227 * 1024, "shared memory");
 };
@@ -196,6 +197,15 @@ struct Walk {
         w.columns = max(16u, (w.n + 15) & ~15u);
         return w;
     }
+    // the same for a warp that is together, in registers the compiler knows to be uniform
+    __device__ __forceinline__ Unit uniform(uint32_t u) {
+        Unit w = at(u);
+        w.expert = __shfl_sync(kFull, w.expert, 0);
+        w.row_unit = __shfl_sync(kFull, w.row_unit, 0);
+        w.first = __shfl_sync(kFull, w.first, 0);
+        w.columns = __shfl_sync(kFull, w.columns, 0);
+        return w;
+    }
 };
 
 // The scale words of four groups of blocks: W's row of scale blocks, and the rows of X that are
@@ -249,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* edge = reinterpret_cast<uint32_t*>(dyn_smem + S::kSmem);  // 2 per expert
     uint32_t* start = edge + 2 * a.g.experts;                           // experts + 1
 
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = P ? blockIdx.x % S::kCtas : 0, first = blockIdx.x / S::kCtas, step = gridDim.x / S::kCtas;
     if (warp == 1) {
         if constexpr (P) {
@@ -306,10 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     sync_ctas<P>();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot, units = start[a.g.experts];
+    // all of the tensor memory is this CTA's, from column 0 (tmem_slot) on
+    constexpr uint32_t tmem = 0;
+    const uint32_t units = __shfl_sync(kFull, start[a.g.experts], 0);
     // Every warp waits together and leaves together.  A wait that runs out ends its warp's loop;
     // the other warps' waits then run out too.
     auto wait = [&](unsigned long long* bar, uint32_t parity) {
+        if (__all_sync(kFull, mbar_poll<P>(bar, parity))) return true;
         if (__all_sync(kFull, mbar_wait<P>(bar, parity))) return true;
         err |= DFX_STATUS_TIMEOUT;
         return false;
@@ -321,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t st = 0, ph = 0, issued = 0;
         bool ok = a.g.inject == 0;  // test hook: the copies are left out
         for (uint32_t u = first; ok && u < units; u += step) {
-            const Unit w = walk.at(u);
+            const Unit w = walk.uniform(u);
             // this CTA's tokens: all, or its half of the columns
             const uint32_t held = w.columns / S::kCtas, token = w.first + rank * held;
             const uint32_t boxes = (held + S::kBox - 1) / S::kBox;
@@ -356,15 +369,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         if (rank == 0) {
-            uint32_t st = 0, ph = 0, slot = 0, slot_ph = 0, acc = 0, acc_ph = 0, unit = 0;
+            uint32_t st = 0, ph = 0, slot = 0, slot_ph = 0, acc = 0, acc_ph = 0, unit = 0, group = 0;
             bool ok = true;
             const uint64_t descA = smem_desc_sw128(tiles), descB = smem_desc_sw128(tiles + kABytes);
             for (uint32_t u = first; ok && u < units; u += step, unit++) {
-                const Unit w = walk.at(u);
+                const Unit w = walk.uniform(u);
                 const uint32_t d = tmem + acc * S::kCap, idesc = idesc_e4m3(w.columns, S::kCtas);
                 if (unit >= 2) ok = wait(&bar_acc_free[acc], acc_ph ^ 1u);
                 for (uint32_t kb0 = 0; ok && kb0 < a.blocks; kb0 += kGroup) {
-                    const uint32_t sf = tmem + S::kScaleColumn + slot * S::kSlotColumns;
+                    // the group before last read the same columns of scales: its MMAs have completed
+                    const uint32_t sf = tmem + S::kScaleColumn + (group % S::kCopies) * S::kSlotColumns;
+                    if (group >= S::kCopies) {
+                        const uint32_t before = group - S::kCopies;
+                        if (!(ok = wait(&bar_scale_free[before % S::kSlots], (before / S::kSlots) & 1u))) break;
+                    }
+                    group++;
                     if (!(ok = wait(&bar_scale[slot], slot_ph))) break;
                     tc_fence_after();
                     if (elect_one()) {
