@@ -89,7 +89,7 @@ int dfx_route(dfx_plan_t plan, const void* d_logits, uint32_t logits_type, uint6
     a.offsets = d_offsets;
     a.rows = d_rows;
     a.slots = d_slots;
-    a.counts = (uint32_t*)d_workspace;
+    a.counts = (uint16_t*)d_workspace;
     return launched(dfx::launch_route(a, stream));
 }
 

@@ -28,9 +28,10 @@ struct RouteArgs {
     int32_t* offsets;       // experts + 1, or NULL: no assignment lists
     int32_t* rows;          // tokens * topk
     int32_t* slots;         // tokens x topk
-    uint32_t* counts;       // workspace: chunks x experts
+    uint16_t* counts;       // workspace: chunks rows of `row` counts (16-byte pieces)
     uint32_t chunk;         // tokens per CTA
-    uint32_t chunks;
+    uint32_t chunks, row;
+    uint32_t whole;         // every lane has its share of experts, in pieces that are aligned
 };
 
 struct QuantizeArgs {

@@ -9,10 +9,13 @@
 // formed in FP64: two experts whose choices are nearer than FP32's rounding would otherwise
 // come in an order that hangs on how a sum was formed.  Ties go to the lowest index.
 //
-// k_route: a warp per token.  Lane i holds the experts i * KPL .. i * KPL + KPL - 1 as unsigned
-// integers in the order of their values (0: not open), so the best is a maximum over the warp
-// (redux), and the lowest lane that has it holds the lowest index.  A CTA takes a chunk of
-// neighbouring tokens and counts its assignments per expert.
+// k_route: a warp per token, a few tokens after one another.  Lane i holds the experts
+// i * KPL .. i * KPL + KPL - 1 as unsigned integers in the order of their values (0: not open), so
+// the best is a maximum over the warp (redux).  Where the logits decide, an expert's index stands
+// in the low bits of its key and the maximum names it; FP64 choices fill their 64 bits, and the
+// lowest lane that has the maximum holds the lowest index.  A warp keeps the picks of 32 / topk
+// tokens, one to a lane, and forms their weights together.  A CTA takes a chunk of neighbouring
+// tokens and counts its assignments per expert.
 // k_place: each CTA sums the counts of the chunks before its own and of all lower experts,
 // then ranks its chunk's assignments: within 32 of them by a match of equal experts, across
 // warps by counts, always in the order of the tokens, so the result does not depend on timing.
@@ -26,15 +29,23 @@
 #include "dfx_common.cuh"
 #include "experts.cuh"
 #include "launch.cuh"
+#include "vec.cuh"
 
 namespace dfx {
 namespace {
 
-constexpr int kRouteThreads = 512;
-constexpr uint32_t kRouteWarps = kRouteThreads / 32;
 constexpr uint32_t kOneChunk = 64;       // tokens that one CTA routes and sorts in one launch
-constexpr uint32_t kChunks = 296;        // chunks of a longer batch: two per SM
-constexpr uint32_t kMaxChunk = 1u << 15; // tokens of a chunk: its counts are 16 bits wide
+constexpr uint32_t kChunks = 148;        // chunks of a longer batch: one per SM
+constexpr uint32_t kMinChunk = 16;       // tokens of a chunk, at least
+constexpr uint32_t kMaxChunk = 1u << 15; // and at most: its counts are 16 bits wide
+constexpr int kPlaceThreads = 512;
+constexpr uint32_t kPlaceWarps = kPlaceThreads / 32;  // warps that rank assignments
+
+// What decides between experts: the logits (BF16 or FP32), or FP64 choices.
+enum Mode { kBf16Logits, kF32Logits, kChoices };
+// FP64 keys, scores and exponentials need registers
+template <int MODE>
+__host__ __device__ constexpr int route_threads() { return MODE == kChoices ? 512 : 1024; }
 
 // unsigned integers in the order of the values; -0 and +0 are the same
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -72,148 +83,239 @@ __device__ __forceinline__ float logit(const RouteArgs& a, uint64_t i) {
     return a.bf16 ? __bfloat162float(((const __nv_bfloat16*)a.logits)[i]) : ((const float*)a.logits)[i];
 }
 
-// One token by one warp: ids and weights.  counts: the CTA's assignments per expert, in shared
-// memory, or NULL.
-template <int KPL, bool WIDE>
-__device__ __forceinline__ void route_token(const RouteArgs& a, uint32_t t, uint32_t* counts) {
-    using Key = typename std::conditional<WIDE, uint64_t, uint32_t>::type;
-    const uint32_t lane = threadIdx.x & 31, e0 = lane * KPL;
-    constexpr float kNone = -INFINITY;
-    float x[KPL];
-    bool open[KPL];
-    float top = kNone;
+// The logits of a token: KPL neighbours per lane, -inf past the last expert.
+template <int KPL>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, uint32_t t, uint32_t e0, float (&x)[KPL]) {
+    const uint64_t at = (uint64_t)t * a.ld + e0;
+    if (a.whole) {  // 32 * KPL experts, rows in whole pieces
+        if (a.bf16) {
+            const __nv_bfloat16* p = (const __nv_bfloat16*)a.logits + at;
+            if constexpr (KPL == 1) {
+                x[0] = __bfloat162float(p[0]);
+            } else if constexpr (KPL == 2) {
+                unpack_bf16(*(const uint32_t*)p, x[0], x[1]);
+            } else if constexpr (KPL == 4) {
+                const uint2 v = *(const uint2*)p;
+                unpack_bf16(v.x, x[0], x[1]), unpack_bf16(v.y, x[2], x[3]);
+            } else {
 #pragma unroll
-    for (int j = 0; j < KPL; j++) {
-        x[j] = e0 + j < a.experts ? logit(a, t * a.ld + e0 + j) : kNone;
-        open[j] = x[j] > kNone;
-        if (open[j]) top = fmaxf(top, x[j]);
+                for (int j = 0; j < KPL; j += 8) {
+                    const uint4 v = *(const uint4*)(p + j);
+                    unpack_bf16(v.x, x[j], x[j + 1]), unpack_bf16(v.y, x[j + 2], x[j + 3]);
+                    unpack_bf16(v.z, x[j + 4], x[j + 5]), unpack_bf16(v.w, x[j + 6], x[j + 7]);
+                }
+            }
+        } else {
+            const float* p = (const float*)a.logits + at;
+            if constexpr (KPL == 1) {
+                x[0] = p[0];
+            } else if constexpr (KPL == 2) {
+                const float2 v = *(const float2*)p;
+                x[0] = v.x, x[1] = v.y;
+            } else {
+#pragma unroll
+                for (int j = 0; j < KPL; j += 4) {
+                    const float4 v = *(const float4*)(p + j);
+                    x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < KPL; j++) x[j] = e0 + j < a.experts ? logit(a, at + j) : -INFINITY;
     }
-    if (!a.sigmoid) top = warp_max(top);
-    Key key[KPL];
-    double denominator = 0.0;
-    if constexpr (WIDE) {
+}
+
+template <int MODE>
+struct KeyOf { using type = uint64_t; };
+template <>
+struct KeyOf<kBf16Logits> { using type = uint32_t; };
+
+// the key of a logit x of expert e where the logits decide; a larger key for a lower index
+__device__ __forceinline__ void logit_key(float x, uint32_t e, uint32_t& key) { key = (ordered(x) & 0xffff0000u) | (0xffffu - e); }
+__device__ __forceinline__ void logit_key(float x, uint32_t e, uint64_t& key) { key = (uint64_t)ordered(x) << 32 | (0xffffu - e); }
+
+// One token by one warp: the keys of its experts, those outside its best groups 0.
+// top, denominator: what its softmax needs.
+template <int KPL, int MODE, class Key>
+__device__ __forceinline__ void token_keys(const RouteArgs& a, const float (&x)[KPL], uint32_t e0, Key (&key)[KPL], float& top,
+                                           double& denominator) {
+    const uint32_t lane = threadIdx.x & 31;
+    constexpr float kNone = -INFINITY;
+    top = kNone;
+    denominator = 0.0;
+    if (!a.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < KPL; j++) top = fmaxf(top, x[j]);  // NaN has no part in it
+        top = warp_max(top);
+    }
+    if constexpr (MODE == kChoices) {
         double s[KPL];
         double sum = 0.0;
 #pragma unroll
         for (int j = 0; j < KPL; j++) {
             s[j] = 0.0;
-            if (open[j]) s[j] = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x[j])) : shifted_exp64(x[j], top);
+            if (x[j] > kNone) s[j] = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x[j])) : shifted_exp64(x[j], top);
             sum += s[j];
         }
         if (!a.sigmoid) {
             denominator = warp_sum(sum);
 #pragma unroll
-            for (int j = 0; j < KPL; j++) s[j] = open[j] ? s[j] / denominator : 0.0;
+            for (int j = 0; j < KPL; j++) s[j] = x[j] > kNone ? s[j] / denominator : 0.0;
         }
 #pragma unroll
         for (int j = 0; j < KPL; j++) {
-            if (a.bias && open[j]) {
-                const float b = *(a.bias + e0 + j);
-                open[j] = b > kNone;
+            bool open = x[j] > kNone;
+            if (a.bias && e0 + j < a.experts) {
+                const float b = a.bias[e0 + j];
+                open = open && b > kNone;
                 s[j] += (double)b;
             }
-            key[j] = open[j] ? ordered(s[j]) : 0;
+            key[j] = open ? ordered(s[j]) : 0;
         }
     } else {
         float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < KPL; j++) key[j] = open[j] ? ordered(x[j]) : 0;
+        for (int j = 0; j < KPL; j++) {
+            logit_key(x[j], e0 + j, key[j]);
+            if (!(x[j] > kNone)) key[j] = 0;
+        }
         if (!a.sigmoid && !a.renormalize) {
 #pragma unroll
-            for (int j = 0; j < KPL; j++) sum += open[j] ? shifted_exp(x[j], top) : 0.0f;
+            for (int j = 0; j < KPL; j++) sum += x[j] > kNone ? shifted_exp(x[j], top) : 0.0f;
             denominator = (double)warp_sum(sum);
         }
     }
 
-    if (a.groups > 1) {
-        // lane g gets group g's score: its best key, or the sum of its best two choices
-        const uint32_t per = a.experts / a.groups;
-        Key mine = 0;
+    if (a.groups <= 1) return;
+    // lane g gets group g's score: its best key, or the sum of its best two choices
+    const uint32_t per = a.experts / a.groups;
+    Key mine = 0;
+    auto score_of = [&](Key best, Key second) {
+        if constexpr (MODE == kChoices)
+            if (a.group_best == 2 && second != 0) return (Key)ordered(value_of(best) + value_of(second));
+        return best;
+    };
+    const uint32_t lanes = per / KPL;
+    if (per % KPL == 0 && (lanes & (lanes - 1)) == 0) {
+        // a group is `lanes` whole lanes: their best two, then an exchange among them
+        Key best = 0, second = 0;
+#pragma unroll
+        for (int j = 0; j < KPL; j++) {
+            second = max(second, min(best, key[j]));
+            best = max(best, key[j]);
+        }
+        for (uint32_t d = 1; d < lanes; d <<= 1) {
+            const Key other = __shfl_xor_sync(kFull, best, d), other2 = __shfl_xor_sync(kFull, second, d);
+            second = max(min(best, other), max(second, other2));
+            best = max(best, other);
+        }
+        mine = __shfl_sync(kFull, score_of(best, second), lane * lanes);  // wraps for lanes past the groups
+    } else {
+        uint32_t group[KPL];
+#pragma unroll
+        for (int j = 0; j < KPL; j++) group[j] = (e0 + j) / per;
         for (uint32_t g = 0; g < a.groups; g++) {
+            Key m = 0, m2 = 0;  // the lane's best two of the group
+#pragma unroll
+            for (int j = 0; j < KPL; j++) {
+                const Key k = group[j] == g ? key[j] : 0;
+                m2 = max(m2, min(m, k));
+                m = max(m, k);
+            }
+            const Key best = warp_max(m);
+            const uint32_t first = __ffs((int)__ballot_sync(kFull, m == best)) - 1;
+            const Key second = warp_max(lane == first ? m2 : m);
+            if (lane == g) mine = score_of(best, second);
+        }
+    }
+    uint32_t above = 0;  // groups that come before lane's
+    for (uint32_t g = 0; g < a.groups; g++) {
+        const Key other = __shfl_sync(kFull, mine, g);
+        above += other > mine || (other == mine && g < lane);
+    }
+    const uint32_t kept = __ballot_sync(kFull, lane < a.groups && above < a.top_groups);
+#pragma unroll
+    for (int j = 0; j < KPL; j++)
+        if (e0 + j < a.experts && !((kept >> ((e0 + j) / per)) & 1u)) key[j] = 0;
+}
+
+// `n` (at most 32 / topk) tokens from t0 on by one warp: ids and weights.  counts: the CTA's
+// assignments per expert, in shared memory, or NULL.
+template <int KPL, int MODE>
+__device__ __forceinline__ void route_tokens(const RouteArgs& a, uint32_t t0, uint32_t n, uint32_t my_token, uint32_t* counts) {
+    using Key = typename KeyOf<MODE>::type;
+    const uint32_t lane = threadIdx.x & 31, e0 = lane * KPL;
+    int id = -1;  // this lane's pick: number lane % topk of token lane / topk
+    float my_top = 0.0f;
+    double my_denominator = 0.0;
+    float x[KPL];
+    load_logits<KPL>(a, t0, e0, x);
+    for (uint32_t i = 0; i < n; i++) {
+        Key key[KPL];
+        float top;
+        double denominator;
+        token_keys<KPL, MODE>(a, x, e0, key, top, denominator);
+        if (i + 1 < n) load_logits<KPL>(a, t0 + i + 1, e0, x);
+        if (my_token == i) my_top = top, my_denominator = denominator;
+        for (uint32_t k = 0; k < a.topk; k++) {
             Key m = 0;
 #pragma unroll
-            for (int j = 0; j < KPL; j++)
-                if ((e0 + j) / per == g && key[j] > m) m = key[j];
+            for (int j = 0; j < KPL; j++) m = max(m, key[j]);
             const Key best = warp_max(m);
-            Key score = best;
-            if constexpr (WIDE) {
-                if (a.group_best == 2 && best != 0) {
-                    // the same again without the first that has it
-                    const uint32_t first = __ffs((int)__ballot_sync(kFull, m == best)) - 1;
-                    Key m2 = 0;
-                    bool dropped = lane != first;
+            if (best == 0) break;
+            int e;
+            if constexpr (MODE == kChoices) {
+                const uint32_t winner = __ffs((int)__ballot_sync(kFull, m == best)) - 1;
+                uint32_t at = 0;
 #pragma unroll
-                    for (int j = 0; j < KPL; j++) {
-                        if ((e0 + j) / per != g) continue;
-                        if (!dropped && key[j] == best) dropped = true;
-                        else if (key[j] > m2) m2 = key[j];
-                    }
-                    const Key second = warp_max(m2);
-                    if (second != 0) score = ordered(value_of(best) + value_of(second));
-                }
+                for (int j = KPL - 1; j >= 0; j--)
+                    if (key[j] == best) at = j;
+#pragma unroll
+                for (int j = 0; j < KPL; j++)
+                    if (lane == winner && at == (uint32_t)j) key[j] = 0;
+                e = (int)(winner * KPL + __shfl_sync(kFull, at, winner));
+            } else {
+                e = 0xffff - (int)((uint32_t)best & 0xffffu);
+#pragma unroll
+                for (int j = 0; j < KPL; j++)
+                    if (key[j] == best) key[j] = 0;
             }
-            if (lane == g) mine = score;
+            if (lane == i * a.topk + k) id = e;
         }
-        uint32_t above = 0;  // groups that come before lane's
-        for (uint32_t g = 0; g < a.groups; g++) {
-            const Key other = __shfl_sync(kFull, mine, g);
-            above += other > mine || (other == mine && g < lane);
-        }
-        const uint32_t kept = __ballot_sync(kFull, lane < a.groups && above < a.top_groups);
-#pragma unroll
-        for (int j = 0; j < KPL; j++)
-            if (e0 + j < a.experts && !((kept >> ((e0 + j) / per)) & 1u)) key[j] = 0;
-    }
-
-    int id = -1;         // of pick number `lane`
-    float chosen = 0.0f; // its logit
-    for (uint32_t k = 0; k < a.topk; k++) {
-        Key m = 0;
-#pragma unroll
-        for (int j = 0; j < KPL; j++) m = max(m, key[j]);
-        const Key best = warp_max(m);
-        if (best == 0) break;
-        const uint32_t winner = __ffs((int)__ballot_sync(kFull, m == best)) - 1;
-        int e = -1;
-        float l = 0.0f;
-        if (lane == winner) {
-#pragma unroll
-            for (int j = KPL - 1; j >= 0; j--)
-                if (key[j] == best) e = j, l = x[j];
-#pragma unroll
-            for (int j = 0; j < KPL; j++)
-                if (j == e) key[j] = 0;
-            e += e0;
-        }
-        e = __shfl_sync(kFull, e, winner);
-        l = __shfl_sync(kFull, l, winner);
-        if (lane == k) id = e, chosen = l;
     }
 
     // the weights, in FP64 and rounded once: one value per lane
     double w = 0.0;
-    if (id >= 0) w = a.sigmoid ? 1.0 / (1.0 + exp(-(double)chosen)) : shifted_exp64(chosen, top);
-    if (a.renormalize) denominator = warp_sum(w);
-    if (a.renormalize || !a.sigmoid) w = denominator > 0.0 ? w / denominator : 0.0;
-    if (lane < a.topk) {
-        const uint64_t o = (uint64_t)t * a.topk + lane;
+    if (id >= 0) {
+        const float chosen = logit(a, (uint64_t)(t0 + my_token) * a.ld + id);
+        w = a.sigmoid ? 1.0 / (1.0 + exp(-(double)chosen)) : shifted_exp64(chosen, my_top);
+    }
+    if (a.renormalize) {
+        my_denominator = 0.0;
+        for (uint32_t k = 0; k < a.topk; k++) my_denominator += __shfl_sync(kFull, w, my_token * a.topk + k);
+    }
+    if (a.renormalize || !a.sigmoid) w = my_denominator > 0.0 ? w / my_denominator : 0.0;
+    if (lane < n * a.topk) {
+        const uint64_t o = (uint64_t)t0 * a.topk + lane;
         a.ids[o] = id;
         a.weights[o] = (float)(w * (double)a.scale);
         if (counts && id >= 0) atomicAdd(counts + id, 1u);
     }
 }
 
-// Slots of the assignments [first, first + n) of a chunk by this CTA, in shared memory
-// base[experts]: the slot of each expert's first assignment of the chunk; warp_base:
-// kRouteWarps x experts, scratch.  Ends with the CTA's warps unsynchronised.
+// Slots of the assignments [first, first + n) of a chunk by this CTA.  In shared memory
+// base[experts]: the slot of each expert's first assignment of the chunk; warp_base: a row of
+// experts for each of the first `warps` warps, scratch.  Ends with the warps unsynchronised.
 __device__ __forceinline__ void place_chunk(const RouteArgs& a, uint32_t first, uint32_t n, const uint32_t* base,
                                             uint16_t* warp_base) {
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // warp w takes the assignments [w * span, (w + 1) * span)
-    const uint32_t span = ((n + kRouteWarps - 1) / kRouteWarps + 31) & ~31u;
+    const uint32_t span = ((n + kPlaceWarps - 1) / kPlaceWarps + 31) & ~31u, warps = n ? (n + span - 1) / span : 0;
     const uint32_t lo = min(n, warp * span), hi = min(n, lo + span);
     uint16_t* mine = warp_base + warp * a.experts;
-    for (uint32_t e = lane; e < a.experts; e += 32) mine[e] = 0;
+    if (warp < warps)
+        for (uint32_t e = lane; e < a.experts; e += 32) mine[e] = 0;
     __syncwarp();
     for (int pass = 0; pass < 2; pass++) {
         for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
@@ -238,9 +340,10 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, uint32_t first, 
         if (pass == 0) {
             // counts of the warps before each, per expert
             __syncthreads();
-            for (uint32_t e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+            for (uint32_t e = threadIdx.x; e < a.experts; e += blockDim.x) {
                 uint32_t sum = 0;
-                for (uint32_t w = 0; w < kRouteWarps; w++) {
+#pragma unroll 4
+                for (uint32_t w = 0; w < warps; w++) {
                     const uint32_t c = warp_base[w * a.experts + e];
                     warp_base[w * a.experts + e] = (uint16_t)sum;
                     sum += c;
@@ -278,103 +381,119 @@ __device__ __forceinline__ void clear_unused(const RouteArgs& a, uint32_t used, 
     for (uint64_t i = (uint64_t)used + thread; i < (uint64_t)a.tokens * a.topk; i += threads) a.rows[i] = -1;
 }
 
-template <int KPL, bool WIDE>
-__global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
+template <int KPL, int MODE>
+__global__ void __launch_bounds__(route_threads<MODE>(), 1) k_route(const RouteArgs a) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     __shared__ uint32_t counts[kMaxExperts], offset[kMaxExperts + 1];
     extern __shared__ __align__(16) uint16_t warp_base[];
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kRouteThreads) counts[e] = 0;
+    constexpr uint32_t kWarps = route_threads<MODE>() / 32;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, my_token = lane / a.topk;
+    for (uint32_t e = threadIdx.x; e < a.experts; e += blockDim.x) counts[e] = 0;
     wait_prior_grid();
     __syncthreads();
     const uint32_t first = blockIdx.x * a.chunk, last = min(a.tokens, first + a.chunk);
-    for (uint32_t t = first + (threadIdx.x >> 5); t < last; t += kRouteWarps)
-        route_token<KPL, WIDE>(a, t, a.offsets ? counts : nullptr);
+    // tokens of a warp at a time: their picks fit its lanes, and every warp has some
+    const uint32_t at_once = min(32 / a.topk, (last - first + kWarps - 1) / kWarps);
+    for (uint32_t t = first + warp * at_once; t < last; t += kWarps * at_once)
+        route_tokens<KPL, MODE>(a, t, min(at_once, last - t), my_token, a.offsets ? counts : nullptr);
     if (!a.offsets) return;
     __syncthreads();
     if (a.chunks > 1) {
-        for (uint32_t e = threadIdx.x; e < a.experts; e += kRouteThreads)
-            a.counts[(uint64_t)blockIdx.x * a.experts + e] = counts[e];
+        for (uint32_t e = threadIdx.x; e < a.row; e += blockDim.x)
+            a.counts[(uint64_t)blockIdx.x * a.row + e] = (uint16_t)(e < a.experts ? counts[e] : 0);
         return;
     }
     scan_experts(counts, offset, a.experts);
-    for (uint32_t e = threadIdx.x; e <= a.experts; e += kRouteThreads) a.offsets[e] = (int32_t)offset[e];
+    for (uint32_t e = threadIdx.x; e <= a.experts; e += blockDim.x) a.offsets[e] = (int32_t)offset[e];
     place_chunk(a, 0, a.tokens * a.topk, offset, warp_base);
-    clear_unused(a, offset[a.experts], threadIdx.x, kRouteThreads);
+    clear_unused(a, offset[a.experts], threadIdx.x, blockDim.x);
 }
 
-__global__ void __launch_bounds__(kRouteThreads) k_place(const RouteArgs a) {
+__global__ void __launch_bounds__(kPlaceThreads) k_place(const RouteArgs a) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     __shared__ uint32_t total[kMaxExperts], before[kMaxExperts], offset[kMaxExperts + 1];
     extern __shared__ __align__(16) uint16_t warp_base[];
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kRouteThreads) total[e] = before[e] = 0;
+    for (uint32_t e = threadIdx.x; e < kMaxExperts; e += kPlaceThreads) total[e] = before[e] = 0;
     __syncthreads();
     wait_prior_grid();
-    // every chunk's counts: thread (e, part) sums a part of the chunks of expert e
-    const uint32_t parts = max(1u, kRouteThreads / a.experts);
-    if (threadIdx.x < parts * a.experts) {
-        const uint32_t e = threadIdx.x % a.experts, part = threadIdx.x / a.experts;
-        uint32_t all = 0, prior = 0;
+    // every chunk's counts, 8 experts to a 16-byte piece: a thread sums some chunks' piece
+    const uint32_t pieces = a.row / 8, parts = kPlaceThreads / pieces;
+    if (threadIdx.x < parts * pieces) {
+        const uint32_t piece = threadIdx.x % pieces;
+        uint32_t all[8] = {}, prior[8] = {};
 #pragma unroll 8
-        for (uint32_t c = part; c < a.chunks; c += parts) {
-            const uint32_t v = a.counts[(uint64_t)c * a.experts + e];
-            all += v;
-            if (c < blockIdx.x) prior += v;
+        for (uint32_t c = threadIdx.x / pieces; c < a.chunks; c += parts) {
+            const uint4 v = *reinterpret_cast<const uint4*>(a.counts + (uint64_t)c * a.row + 8 * piece);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w}, mine = c < blockIdx.x ? 0xffffffffu : 0u;
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const uint32_t n = (w[j / 2] >> (16 * (j & 1))) & 0xffffu;
+                all[j] += n;
+                prior[j] += n & mine;
+            }
         }
-        atomicAdd(total + e, all);
-        atomicAdd(before + e, prior);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            if (all[j]) atomicAdd(total + 8 * piece + j, all[j]);
+            if (prior[j]) atomicAdd(before + 8 * piece + j, prior[j]);
+        }
     }
     __syncthreads();
     scan_experts(total, offset, a.experts);
     if (blockIdx.x == 0)
-        for (uint32_t e = threadIdx.x; e <= a.experts; e += kRouteThreads) a.offsets[e] = (int32_t)offset[e];
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kRouteThreads) before[e] += offset[e];
+        for (uint32_t e = threadIdx.x; e <= a.experts; e += kPlaceThreads) a.offsets[e] = (int32_t)offset[e];
+    for (uint32_t e = threadIdx.x; e < a.experts; e += kPlaceThreads) before[e] += offset[e];
     __syncthreads();
     const uint32_t first = blockIdx.x * a.chunk, last = min(a.tokens, first + a.chunk);
     place_chunk(a, first * a.topk, (last - first) * a.topk, before, warp_base);
-    clear_unused(a, offset[a.experts], blockIdx.x * kRouteThreads + threadIdx.x, gridDim.x * kRouteThreads);
+    clear_unused(a, offset[a.experts], blockIdx.x * kPlaceThreads + threadIdx.x, gridDim.x * kPlaceThreads);
 }
 
 uint32_t chunk_tokens(uint64_t tokens) {
     if (tokens <= kOneChunk) return kOneChunk;
-    const uint64_t per = (tokens + kChunks - 1) / kChunks;
-    const uint64_t chunk = (per + kRouteWarps - 1) / kRouteWarps * kRouteWarps;
-    return (uint32_t)(chunk < kMaxChunk ? chunk : kMaxChunk);
+    const uint64_t chunk = (tokens + kChunks - 1) / kChunks;
+    return (uint32_t)(chunk < kMinChunk ? kMinChunk : chunk < kMaxChunk ? chunk : kMaxChunk);
 }
+uint32_t count_row(uint32_t experts) { return (experts + 7) & ~7u; }
 
-template <bool WIDE>
+template <int MODE>
 cudaError_t launch(const RouteArgs& a, size_t smem, cudaStream_t s) {
     const int grid = (int)a.chunks;
-    auto go = [&](auto* k, bool* attr_set) {
-        const cudaError_t e = allow_smem(k, kRouteWarps * kMaxExperts * sizeof(uint16_t), attr_set);
-        return e != cudaSuccess ? e : launch_programmatic(k, grid, kRouteThreads, smem, s, a);
-    };
     static bool set[5][64] = {};
-    if (a.experts <= 32) return go(k_route<1, WIDE>, set[0]);
-    if (a.experts <= 64) return go(k_route<2, WIDE>, set[1]);
-    if (a.experts <= 128) return go(k_route<4, WIDE>, set[2]);
-    if (a.experts <= 256) return go(k_route<8, WIDE>, set[3]);
-    return go(k_route<16, WIDE>, set[4]);
+    auto go = [&](auto* k, bool* attr_set) {
+        const cudaError_t e = allow_smem(k, kPlaceWarps * kMaxExperts * sizeof(uint16_t), attr_set);
+        return e != cudaSuccess ? e : launch_programmatic(k, grid, route_threads<MODE>(), smem, s, a);
+    };
+    if (a.experts <= 32) return go(k_route<1, MODE>, set[0]);
+    if (a.experts <= 64) return go(k_route<2, MODE>, set[1]);
+    if (a.experts <= 128) return go(k_route<4, MODE>, set[2]);
+    if (a.experts <= 256) return go(k_route<8, MODE>, set[3]);
+    return go(k_route<16, MODE>, set[4]);
 }
 
 }  // namespace
 
 uint64_t route_workspace_bytes(uint64_t tokens, uint32_t experts) {
     const uint64_t chunk = chunk_tokens(tokens), chunks = (tokens + chunk - 1) / chunk;
-    return align16(4 * (chunks > 1 ? chunks * experts : 4));
+    return align16(2 * (chunks > 1 ? chunks * count_row(experts) : 8));
 }
 
 cudaError_t launch_route(RouteArgs a, cudaStream_t s) {
     a.chunk = chunk_tokens(a.tokens);
     a.chunks = (a.tokens + a.chunk - 1) / a.chunk;
     if (a.chunks == 0) a.chunks = 1;  // no token: the offsets are still written
-    const size_t smem = kRouteWarps * a.experts * sizeof(uint16_t);
+    a.row = count_row(a.experts);
+    const uint32_t lane_experts = (a.experts + 31) / 32, bytes = a.bf16 ? 2 : 4;
+    a.whole = a.experts % 32 == 0 && (lane_experts & (lane_experts - 1)) == 0 && a.ld * bytes % 16 == 0;
+    const size_t smem = kPlaceWarps * a.experts * sizeof(uint16_t), first = a.chunks == 1 && a.offsets ? smem : 0;
     // FP64 choices where a bias or a sum decides; else the logits' own order
-    const bool wide = a.bias || (a.groups > 1 && a.group_best == 2);
-    cudaError_t e = wide ? launch<true>(a, a.chunks == 1 ? smem : 0, s) : launch<false>(a, a.chunks == 1 ? smem : 0, s);
+    cudaError_t e = a.bias || (a.groups > 1 && a.group_best == 2) ? launch<kChoices>(a, first, s)
+                    : a.bf16                                      ? launch<kBf16Logits>(a, first, s)
+                                                                  : launch<kF32Logits>(a, first, s);
     if (e != cudaSuccess || !a.offsets || a.chunks == 1) return e;
     static bool set[64] = {};
-    e = allow_smem(k_place, kRouteWarps * kMaxExperts * sizeof(uint16_t), set);
-    return e != cudaSuccess ? e : launch_programmatic(k_place, (int)a.chunks, kRouteThreads, smem, s, a);
+    e = allow_smem(k_place, kPlaceWarps * kMaxExperts * sizeof(uint16_t), set);
+    return e != cudaSuccess ? e : launch_programmatic(k_place, (int)a.chunks, kPlaceThreads, smem, s, a);
 }
 
 }  // namespace dfx
