@@ -9,8 +9,10 @@ lossless_entropy_coded_exponent_b200.build``) or a call fails.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdfx.so")
@@ -386,3 +388,206 @@ def decode(comp, n: int, plan: Plan | None = None, out=None, stream=None, check:
     finally:
         if own:
             plan.free()
+
+
+# Layers of experts with 8-bit weights.  These run on the tensors' device and on its current
+# torch stream (or `stream`, a torch stream: then what they allocate belongs to it).  A plan of
+# the device may be passed in; without one a call makes its own, waits for the work and raises
+# if its status word says that an index was out of range or a wait ran out.
+
+class Fp8(NamedTuple):
+    """e4m3 values and e8m0 block scales (include/dfx.h): uint8 tensors [..., rows, ld]."""
+    values: "torch.Tensor"
+    scales: "torch.Tensor"
+    cols: int         # values of a row
+    block_rows: int   # 1, or 128 (weights)
+
+
+class Routing(NamedTuple):
+    """What dfx_route gives: experts and weights [tokens, topk]; where the assignments of each
+    expert begin [experts + 1], their tokens [tokens * topk], and each assignment's place."""
+    ids: "torch.Tensor"
+    weights: "torch.Tensor"
+    offsets: "torch.Tensor"
+    rows: "torch.Tensor"
+    slots: "torch.Tensor"
+
+
+@contextlib.contextmanager
+def _call(tensor, plan, stream, what):
+    """Device, stream and plan of a helper's calls: yields (plan, stream handle)."""
+    import torch
+
+    if not tensor.is_cuda:
+        raise ValueError(f"{what}: tensors must be on a CUDA device (there is no CPU fallback)")
+    with torch.cuda.device(tensor.device), torch.cuda.stream(stream):
+        handle = torch.cuda.current_stream().cuda_stream
+        own = plan is None
+        if own:
+            plan = dfx_plan(0)
+        try:
+            yield plan, handle
+            if own:
+                st = dfx_device_status(plan, stream=handle)
+                if st:
+                    raise DfxError(DFX_ERR_CORRUPT, f"{what} (device status 0x{st:x})")
+        finally:
+            if own:
+                plan.free()
+
+
+def _float_type(t, what: str) -> int:
+    import torch
+
+    if t not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{what}: float32 or bfloat16, not {t}")
+    return DFX_F32 if t == torch.float32 else DFX_BF16
+
+
+def _matrix(x, what: str):
+    """A 2-D tensor whose rows the library can read: neighbouring elements, 16-byte aligned."""
+    if x.dim() != 2:
+        raise ValueError(f"{what}: a matrix is needed, not {x.dim()} dimensions")
+    return x if x.stride(1) == 1 and x.stride(0) >= x.shape[1] and x.data_ptr() % 16 == 0 else x.clone(
+        memory_format=_contiguous())
+
+
+def _contiguous():
+    import torch
+
+    return torch.contiguous_format
+
+
+def _ld(x) -> int:
+    return max(x.stride(0), x.shape[1])
+
+
+def _same_device(what: str, *tensors):
+    if len({t.device for t in tensors if t is not None}) > 1:
+        raise ValueError(f"{what}: tensors on different devices")
+
+
+def route(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+          group_best: int = 1, renormalize: bool = False, scale: float = 1.0, plan: Plan | None = None,
+          stream=None) -> Routing:
+    """Each token's best experts (dfx_route) from gate logits [tokens, experts]."""
+    import torch
+
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError("route: score is 'softmax' or 'sigmoid'")
+    kind = _float_type(logits.dtype, "route")
+    _same_device("route", logits, bias)
+    with _call(logits, plan, stream, "route") as (p, s):
+        x = _matrix(logits, "route")
+        tokens, experts = x.shape
+        if bias is not None:
+            if bias.shape != (experts,):
+                raise ValueError("route: a bias for each expert")
+            bias = bias.to(torch.float32).clone()  # aligned, whatever it was a part of
+        params = dfx_route_params(score=DFX_SCORE_SIGMOID if score == "sigmoid" else DFX_SCORE_SOFTMAX, topk=topk,
+                                  groups=groups, top_groups=top_groups, group_best=group_best,
+                                  renormalize=int(renormalize), scale=scale)
+        ints = lambda *shape: torch.empty(shape, dtype=torch.int32, device=x.device)  # noqa: E731
+        work = torch.empty(dfx_route_workspace(tokens, experts, params), dtype=torch.uint8, device=x.device)
+        out = Routing(ints(tokens, topk), torch.empty(tokens, topk, device=x.device), ints(experts + 1),
+                      ints(tokens * topk), ints(tokens, topk))
+        dfx_route(p, x, kind, _ld(x), tokens, experts, bias, params, *out, work, work.numel(), stream=s)
+    return out
+
+
+def quantize_fp8(x, block_rows: int = 1, index=None, swiglu: bool = False, plan: Plan | None = None,
+                 stream=None) -> Fp8:
+    """e4m3 values and block scales (dfx_quantize_fp8) of x [rows, cols], or of each matrix of
+    x [experts, rows, cols].  index (int32): output row r is x[index[r]], a row with a negative
+    index is not written; swiglu: x holds gates, then values, in each row."""
+    import torch
+
+    kind = _float_type(x.dtype, "quantize_fp8")
+    if x.dim() not in (2, 3) or (x.dim() == 3 and (index is not None or swiglu)):
+        raise ValueError("quantize_fp8: a matrix, or several of them without index and swiglu")
+    if swiglu and x.shape[-1] % 2:
+        raise ValueError("quantize_fp8: as many gates as values")
+    if index is not None and (index.dim() != 1 or index.dtype != torch.int32):
+        raise TypeError("quantize_fp8: index is a vector of int32")
+    _same_device("quantize_fp8", x, index)
+    cols = x.shape[-1] // 2 if swiglu else x.shape[-1]
+    rows = x.shape[-2] if index is None else index.numel()
+    blocks = -(-cols // 128)
+    with _call(x, plan, stream, "quantize_fp8") as (p, s):
+        q = torch.empty(*x.shape[:-2], rows, -(-cols // 16) * 16, dtype=torch.uint8, device=x.device)
+        # rows of scales in 16-byte pieces, which the product loads faster
+        sc = torch.empty(*x.shape[:-2], -(-rows // block_rows), -(-blocks // 16) * 16, dtype=torch.uint8, device=x.device)
+        if index is not None:
+            index = index if index.is_contiguous() and index.data_ptr() % 16 == 0 else index.clone()
+        for part, pq, ps in zip(x, q, sc) if x.dim() == 3 else ((x, q, sc),):
+            m = _matrix(part, "quantize_fp8")
+            dfx_quantize_fp8(p, m, kind, _ld(m), m.shape[0], index, rows, cols, block_rows,
+                             DFX_QUANT_SWIGLU if swiglu else 0, pq, q.shape[-1], ps, sc.shape[-1], stream=s)
+    return Fp8(q, sc, cols, block_rows)
+
+
+def gemm_fp8(x: Fp8, w: Fp8, offsets=None, dtype=None, out=None, plan: Plan | None = None, stream=None):
+    """x w^T (dfx_gemm_fp8): x [tokens, cols]; w [rows, cols], or [experts, rows, cols] with
+    offsets (int32 [experts + 1]): expert e has x's rows offsets[e] .. offsets[e + 1] - 1, and rows
+    that no expert has are not written.  dtype: bfloat16 (default) or float32; out: a matrix to
+    write into."""
+    import torch
+
+    if x.block_rows != 1 or w.block_rows != 128 or x.values.dim() != 2 or w.values.dim() not in (2, 3):
+        raise ValueError("gemm_fp8: x in blocks of 1 x 128, w in blocks of 128 x 128")
+    if x.cols != w.cols:
+        raise ValueError(f"gemm_fp8: rows of {x.cols} and of {w.cols} values")
+    experts = w.values.shape[0] if w.values.dim() == 3 else 1
+    if offsets is not None and (offsets.dtype != torch.int32 or offsets.shape != (experts + 1,) or not offsets.is_contiguous()):
+        raise ValueError("gemm_fp8: offsets is an int32 vector of one more than the experts")
+    _same_device("gemm_fp8", x.values, x.scales, w.values, w.scales, offsets, out)
+    if out is not None and (out.dim() != 2 or out.stride(1) != 1 or out.shape != (x.values.shape[0], w.values.shape[-2])
+                            or (dtype is not None and out.dtype != dtype)):
+        raise ValueError("gemm_fp8: out is a [tokens, rows] matrix with neighbouring elements")
+    dtype = out.dtype if out is not None else dtype or torch.bfloat16
+    kind = _float_type(dtype, "gemm_fp8")
+    with _call(x.values, plan, stream, "gemm_fp8") as (p, s):
+        tokens, rows = x.values.shape[0], w.values.shape[-2]
+        y = torch.empty(tokens, rows, dtype=dtype, device=x.values.device) if out is None else out
+        dfx_gemm_fp8(p, x.values, x.values.shape[-1], x.scales, x.scales.shape[-1], tokens, w.values, w.values.shape[-1],
+                     w.scales, w.scales.shape[-1], rows, x.cols, experts, offsets, y, kind, _ld(y), stream=s)
+    return y
+
+
+def combine(z, slots, weights, dtype=None, plan: Plan | None = None, stream=None):
+    """y[t] = sum over k of weights[t, k] z[slots[t, k]] (dfx_combine); a negative slot adds
+    nothing.  dtype: that of z (default), bfloat16 or float32."""
+    import torch
+
+    dtype = dtype or z.dtype
+    kind, y_kind = _float_type(z.dtype, "combine"), _float_type(dtype, "combine")
+    if slots.shape != weights.shape or slots.dim() != 2 or slots.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise ValueError("combine: int32 slots and float32 weights [tokens, topk]")
+    _same_device("combine", z, slots, weights)
+    with _call(z, plan, stream, "combine") as (p, s):
+        m = _matrix(z, "combine")
+        slots, weights = (t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=_contiguous())
+                          for t in (slots, weights))
+        y = torch.empty(slots.shape[0], m.shape[1], dtype=dtype, device=z.device)
+        dfx_combine(p, m, kind, _ld(m), m.shape[0], m.shape[1], slots, weights, slots.shape[0], slots.shape[1], y, y_kind,
+                    _ld(y), stream=s)
+    return y
+
+
+def experts_fp8(x, logits, w_in: Fp8, w_out: Fp8, topk: int, plan: Plan | None = None, stream=None, **routing):
+    """A mixture-of-experts feed-forward layer with 8-bit weights: for each token the weighted sum
+    over its experts of w_out (silu(gate) * value), where [gate, value] = w_in x.
+      x [tokens, width], logits [tokens, experts] (a row of -inf: padding, zeros come out);
+      w_in: quantize_fp8 of [experts, 2 * inner, width] in 128-row blocks (gates first), w_out of
+      [experts, width, inner]; routing: route's keywords.  The result has x's type."""
+    import torch
+
+    _same_device("experts_fp8", x, logits, w_in.values, w_out.values)
+    with _call(x, plan, stream, "experts_fp8") as (p, _):
+        r = route(logits, topk, plan=p, **routing)
+        # the tokens in the experts' order, an expert's rows beside one another
+        xq = quantize_fp8(x, index=r.rows, plan=p)
+        h = gemm_fp8(xq, w_in, r.offsets, dtype=torch.bfloat16, plan=p)
+        hq = quantize_fp8(h, swiglu=True, plan=p)
+        z = gemm_fp8(hq, w_out, r.offsets, dtype=torch.bfloat16, plan=p)
+        return combine(z, r.slots, r.weights, dtype=x.dtype, plan=p)

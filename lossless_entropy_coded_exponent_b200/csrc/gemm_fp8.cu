@@ -392,7 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     // all of the tensor memory is this CTA's, from column 0 (tmem_slot) on
     constexpr uint32_t tmem = 0;
-    const uint32_t units = __shfl_sync(kFull, start[a.g.experts], 0);
+    // (of a split, one unit to a cluster: offsets out of order could count rows twice)
+    const uint32_t all_units = __shfl_sync(kFull, start[a.g.experts], 0), units = ctas > S::kCtas ? min(all_units, step) : all_units;
     // Every warp waits together and leaves together.  A wait that runs out ends its warp's loop;
     // the other warps' waits then run out too.
     auto wait = [&](unsigned long long* bar, uint32_t parity) {

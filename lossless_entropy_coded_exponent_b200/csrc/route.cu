@@ -43,9 +43,9 @@ constexpr uint32_t kPlaceWarps = kPlaceThreads / 32;  // warps that rank assignm
 
 // What decides between experts: the logits (BF16 or FP32), or FP64 choices.
 enum Mode { kBf16Logits, kF32Logits, kChoices };
-// FP64 keys, scores and exponentials need registers
-template <int MODE>
-__host__ __device__ constexpr int route_threads() { return MODE == kChoices ? 512 : 1024; }
+// A warp's tokens are a chain of dependent steps, so the SM wants many warps: with 512 threads and no
+// spills 4096 tokens over 256 experts took 22.8 us, with 1024 they take 20.5.
+constexpr int kRouteThreads = 1024;
 
 // unsigned integers in the order of the values; -0 and +0 are the same
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -240,6 +240,101 @@ __device__ __forceinline__ void token_keys(const RouteArgs& a, const float (&x)[
         if (e0 + j < a.experts && !((kept >> ((e0 + j) / per)) & 1u)) key[j] = 0;
 }
 
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float((key >> 31) ? key & 0x7fffffffu : ~key);
+}
+
+// The picks of one token whose choices are sums, in FP32: true if no two choices (or groups) that
+// decide are nearer than their rounding.  An error is at most 2^-21 of 1 + |choice| for a sigmoid
+// (exponential 2^-22, sum and quotient 2^-24 each, the bias' sum 2^-24), and 2^-19 for a softmax
+// (up to 21 additions of 2^-24 more), and the key's last bits, given to its place in the lane, are
+// 2^-20 of the choice; a difference is trusted from 2^-18 and 2^-16 on.  Lane first_lane + k gets
+// pick k in id.
+template <int KPL>
+__device__ __forceinline__ bool quick_picks(const RouteArgs& a, const float (&x)[KPL], uint32_t e0, uint32_t first_lane, float& top,
+                                            double& denominator, int& id) {
+    const uint32_t lane = threadIdx.x & 31;
+    constexpr float kNone = -INFINITY;
+    const float tolerance = a.sigmoid ? 0x1p-18f : 0x1p-16f;
+    uint32_t key[KPL];
+    float sum = 0.0f;
+    top = kNone;
+    if (!a.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < KPL; j++) top = fmaxf(top, x[j]);
+        top = warp_max(top);
+#pragma unroll
+        for (int j = 0; j < KPL; j++) sum += x[j] > kNone ? shifted_exp(x[j], top) : 0.0f;
+        sum = warp_sum(sum);
+    }
+    denominator = (double)sum;
+#pragma unroll
+    for (int j = 0; j < KPL; j++) {
+        bool open = x[j] > kNone;
+        float c = a.sigmoid ? 1.0f / (1.0f + expf(-x[j])) : shifted_exp(x[j], top) / sum;
+        if (a.bias && e0 + j < a.experts) {
+            const float b = a.bias[e0 + j];
+            open = open && b > kNone;
+            c += b;
+        }
+        // the last bits name the key within its lane
+        key[j] = open ? (ordered(c) & ~(uint32_t)(KPL - 1)) | (KPL - 1 - j) : 0;
+    }
+    bool sure = true;
+    if (a.groups > 1) {
+        const uint32_t per = a.experts / a.groups, lanes = per / KPL;
+        if (per % KPL != 0 || (lanes & (lanes - 1)) != 0) return false;  // a group is no run of whole lanes
+        uint32_t best = 0, second = 0;
+#pragma unroll
+        for (int j = 0; j < KPL; j++) {
+            second = max(second, min(best, key[j]));
+            best = max(best, key[j]);
+        }
+        for (uint32_t d = 1; d < lanes; d <<= 1) {
+            const uint32_t other = __shfl_xor_sync(kFull, best, d), other2 = __shfl_xor_sync(kFull, second, d);
+            second = max(min(best, other), max(second, other2));
+            best = max(best, other);
+        }
+        const uint32_t score = a.group_best == 2 && second != 0 ? ordered(value_of(best) + value_of(second)) : best;
+        const uint32_t mine = __shfl_sync(kFull, score, lane * lanes);
+        uint32_t above = 0;
+        for (uint32_t g = 0; g < a.groups; g++) {
+            const uint32_t other = __shfl_sync(kFull, mine, g);
+            above += other > mine || (other == mine && g < lane);
+        }
+        const bool inside = lane < a.groups, keep = inside && above < a.top_groups;
+        const uint32_t kept = __ballot_sync(kFull, keep);
+        const uint32_t low = __reduce_min_sync(kFull, keep ? mine : 0xffffffffu);
+        const uint32_t high = warp_max(inside && !keep ? mine : 0u);
+        if (high != 0) {
+            const float l = value_of(low), h = value_of(high);
+            sure = l - h > 2.0f * tolerance * (1.0f + fabsf(h));
+        }
+        if (!((kept >> (lane / lanes)) & 1u)) {
+#pragma unroll
+            for (int j = 0; j < KPL; j++) key[j] = 0;
+        }
+    }
+    float last = 0.0f;
+    for (uint32_t k = 0; k <= a.topk; k++) {  // one more than is picked: the last must stand clear too
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < KPL; j++) m = max(m, key[j]);
+        const uint32_t best = warp_max(m);
+        if (best == 0) break;
+        const float c = value_of(best);
+        const uint32_t who = __ballot_sync(kFull, m == best);
+        sure = sure && (who & (who - 1)) == 0 && (k == 0 || last - c > tolerance * (1.0f + fabsf(c)));
+        last = c;
+#pragma unroll
+        for (int j = 0; j < KPL; j++)
+            if (key[j] == best) key[j] = 0;
+        const int e = (__ffs((int)who) - 1) * KPL + (KPL - 1 - (int)(best & (KPL - 1)));
+        if (k < a.topk && lane == first_lane + k) id = e;
+    }
+    return sure;
+}
+
 // `n` (at most 32 / topk) tokens from t0 on by one warp: ids and weights.  counts: the CTA's
 // assignments per expert, in shared memory, or NULL.
 template <int KPL, int MODE>
@@ -255,6 +350,14 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, uint32_t t0, ui
         Key key[KPL];
         float top;
         double denominator;
+        if constexpr (MODE == kChoices) {
+            if (quick_picks<KPL>(a, x, e0, i * a.topk, top, denominator, id)) {
+                if (i + 1 < n) load_logits<KPL>(a, t0 + i + 1, e0, x);
+                if (my_token == i) my_top = top, my_denominator = denominator;
+                continue;
+            }
+            if (my_token == i) id = -1;
+        }
         token_keys<KPL, MODE>(a, x, e0, key, top, denominator);
         if (i + 1 < n) load_logits<KPL>(a, t0 + i + 1, e0, x);
         if (my_token == i) my_top = top, my_denominator = denominator;
@@ -304,74 +407,95 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, uint32_t t0, ui
     }
 }
 
-// Slots of the assignments [first, first + n) of a chunk by this CTA.  In shared memory
-// base[experts]: the slot of each expert's first assignment of the chunk; warp_base: a row of
-// experts for each of the first `warps` warps, scratch.  Ends with the warps unsynchronised.
-__device__ __forceinline__ void place_chunk(const RouteArgs& a, uint32_t first, uint32_t n, const uint32_t* base,
-                                            uint16_t* warp_base) {
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // warp w takes the assignments [w * span, (w + 1) * span)
-    const uint32_t span = ((n + kPlaceWarps - 1) / kPlaceWarps + 31) & ~31u, warps = n ? (n + span - 1) / span : 0;
-    const uint32_t lo = min(n, warp * span), hi = min(n, lo + span);
-    uint16_t* mine = warp_base + warp * a.experts;
-    if (warp < warps)
+// The ranking of a chunk's assignments [first, first + n) by the CTA's first kPlaceWarps warps, warp
+// w those of its span.  count() ranks each among the warp's of the same expert and leaves the
+// warp's counts in warp_base (a row of experts for each warp with a span); place() turns the
+// counts into starts and writes the slots, from base[experts], the slot of each expert's first
+// assignment of the chunk.  Every thread of the CTA calls both, with a barrier in between.
+struct Ranking {
+    static constexpr uint32_t kHeld = 8;  // rounds of 32 whose ranks stay in registers
+    const RouteArgs& a;
+    uint32_t first, n, warps, lo, hi;
+    uint32_t held[kHeld];  // expert << 16 | rank
+    __device__ __forceinline__ Ranking(const RouteArgs& a_, uint32_t first_, uint32_t n_) : a(a_), first(first_), n(n_) {
+        const uint32_t warp = threadIdx.x >> 5, span = ((n + kPlaceWarps - 1) / kPlaceWarps + 31) & ~31u;
+        warps = n ? (n + span - 1) / span : 0;
+        lo = min(n, warp * span);
+        hi = min(n, lo + span);
+    }
+    __device__ __forceinline__ uint32_t rank(uint32_t i, uint16_t* mine) {
+        const uint32_t lane = threadIdx.x & 31;
+        const int e = i < hi ? a.ids[first + i] : -1;
+        const uint32_t peers = __match_any_sync(kFull, e), before = __popc(peers & ((1u << lane) - 1u));
+        uint32_t at = 0;
+        if (e >= 0) at = mine[e];
+        __syncwarp();
+        if (e >= 0 && before == 0) mine[e] = (uint16_t)(at + __popc(peers));
+        __syncwarp();
+        return e >= 0 ? (uint32_t)e << 16 | (at + before) : 0xffffffffu;
+    }
+    __device__ __forceinline__ void count(uint16_t* warp_base) {
+        const uint32_t lane = threadIdx.x & 31;
+        uint16_t* mine = warp_base + (threadIdx.x >> 5) * a.experts;
+        if (lo >= hi) return;  // the same for the warp
         for (uint32_t e = lane; e < a.experts; e += 32) mine[e] = 0;
-    __syncwarp();
-    for (int pass = 0; pass < 2; pass++) {
-        for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
-            const uint32_t i = i0 + lane;
-            const int e = i < hi ? a.ids[first + i] : -1;
-            const uint32_t peers = __match_any_sync(kFull, e);
-            const uint32_t before = __popc(peers & ((1u << lane) - 1u));
-            uint32_t at = 0;
-            if (e >= 0) at = mine[e];
-            __syncwarp();
-            if (e >= 0 && before == 0) mine[e] = (uint16_t)(at + __popc(peers));
-            __syncwarp();
-            if (pass == 1 && i < hi) {
-                int slot = -1;
-                if (e >= 0) {
-                    slot = (int)(base[e] + at + before);
-                    a.rows[slot] = (int32_t)((first + i) / a.topk);
-                }
-                a.slots[first + i] = slot;
-            }
-        }
-        if (pass == 0) {
-            // counts of the warps before each, per expert
-            __syncthreads();
-            for (uint32_t e = threadIdx.x; e < a.experts; e += blockDim.x) {
-                uint32_t sum = 0;
-#pragma unroll 4
-                for (uint32_t w = 0; w < warps; w++) {
-                    const uint32_t c = warp_base[w * a.experts + e];
-                    warp_base[w * a.experts + e] = (uint16_t)sum;
-                    sum += c;
-                }
-            }
-            __syncthreads();
+        __syncwarp();
+#pragma unroll
+        for (uint32_t k = 0; k < kHeld; k++)
+            if (lo + 32 * k < hi) held[k] = rank(lo + 32 * k + lane, mine);
+        for (uint32_t i = lo + 32 * kHeld + lane; i - lane < hi; i += 32) {
+            const uint32_t r = rank(i, mine);
+            if (i < hi) a.slots[first + i] = (int32_t)r;  // kept there for place()
         }
     }
-}
-
-// Exclusive sum over the experts of total[] (shared, experts <= 512) into offset[experts + 1];
-// every thread calls it.
-__device__ __forceinline__ void scan_experts(const uint32_t* total, uint32_t* offset, uint32_t experts) {
-    const uint32_t lane = threadIdx.x & 31;
-    if (threadIdx.x < 32) {
-        uint32_t carry = 0;
-        for (uint32_t e0 = 0; e0 < experts; e0 += 32) {
-            const uint32_t v = e0 + lane < experts ? total[e0 + lane] : 0;
-            uint32_t incl = v;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t y = __shfl_up_sync(kFull, incl, d);
-                if (lane >= (uint32_t)d) incl += y;
-            }
-            if (e0 + lane < experts) offset[e0 + lane] = carry + incl - v;
-            carry += __shfl_sync(kFull, incl, 31);
+    __device__ __forceinline__ void write(uint32_t i, uint32_t r, const uint32_t* base, const uint16_t* mine) {
+        if (i >= hi) return;
+        int slot = -1;
+        if (r != 0xffffffffu) {
+            slot = (int)(base[r >> 16] + mine[r >> 16] + (r & 0xffffu));
+            a.rows[slot] = (int32_t)((first + i) / a.topk);
         }
-        if (lane == 0) offset[experts] = carry;
+        a.slots[first + i] = slot;
+    }
+    __device__ __forceinline__ void place(const uint32_t* base, uint16_t* warp_base) {
+        for (uint32_t e = threadIdx.x; e < a.experts; e += blockDim.x) {
+            uint32_t sum = 0;
+#pragma unroll 4
+            for (uint32_t w = 0; w < warps; w++) {
+                const uint32_t c = warp_base[w * a.experts + e];
+                warp_base[w * a.experts + e] = (uint16_t)sum;
+                sum += c;
+            }
+        }
+        __syncthreads();
+        const uint32_t lane = threadIdx.x & 31;
+        const uint16_t* mine = warp_base + (threadIdx.x >> 5) * a.experts;
+#pragma unroll
+        for (uint32_t k = 0; k < kHeld; k++)
+            if (lo + 32 * k < hi) write(lo + 32 * k + lane, held[k], base, mine);
+        for (uint32_t i = lo + 32 * kHeld + lane; i < hi; i += 32) write(i, (uint32_t)a.slots[first + i], base, mine);
+    }
+};
+
+// Exclusive sum over the experts of total[] (shared, experts <= 512, the CTA at least as wide) into
+// offset[experts + 1]; every thread calls it, between barriers of its own.
+__device__ __forceinline__ void scan_experts(const uint32_t* total, uint32_t* offset, uint32_t experts) {
+    __shared__ uint32_t warp_sum[kMaxExperts / 32];
+    const uint32_t e = threadIdx.x, lane = e & 31;
+    const uint32_t v = e < experts ? total[e] : 0;
+    uint32_t incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(kFull, incl, d);
+        if (lane >= (uint32_t)d) incl += y;
+    }
+    if (lane == 31 && e < kMaxExperts) warp_sum[e / 32] = incl;
+    __syncthreads();
+    if (e < experts) {
+        uint32_t before = 0;
+        for (uint32_t w = 0; w < e / 32; w++) before += warp_sum[w];
+        offset[e] = before + incl - v;
+        if (e + 1 == experts) offset[experts] = before + incl;
     }
     __syncthreads();
 }
@@ -382,11 +506,11 @@ __device__ __forceinline__ void clear_unused(const RouteArgs& a, uint32_t used, 
 }
 
 template <int KPL, int MODE>
-__global__ void __launch_bounds__(route_threads<MODE>(), 1) k_route(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, 1) k_route(const RouteArgs a) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     __shared__ uint32_t counts[kMaxExperts], offset[kMaxExperts + 1];
     extern __shared__ __align__(16) uint16_t warp_base[];
-    constexpr uint32_t kWarps = route_threads<MODE>() / 32;
+    constexpr uint32_t kWarps = kRouteThreads / 32;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, my_token = lane / a.topk;
     for (uint32_t e = threadIdx.x; e < a.experts; e += blockDim.x) counts[e] = 0;
     wait_prior_grid();
@@ -403,9 +527,11 @@ __global__ void __launch_bounds__(route_threads<MODE>(), 1) k_route(const RouteA
             a.counts[(uint64_t)blockIdx.x * a.row + e] = (uint16_t)(e < a.experts ? counts[e] : 0);
         return;
     }
+    Ranking ranking(a, 0, a.tokens * a.topk);
+    ranking.count(warp_base);
     scan_experts(counts, offset, a.experts);
     for (uint32_t e = threadIdx.x; e <= a.experts; e += blockDim.x) a.offsets[e] = (int32_t)offset[e];
-    place_chunk(a, 0, a.tokens * a.topk, offset, warp_base);
+    ranking.place(offset, warp_base);
     clear_unused(a, offset[a.experts], threadIdx.x, blockDim.x);
 }
 
@@ -416,14 +542,24 @@ __global__ void __launch_bounds__(kPlaceThreads) k_place(const RouteArgs a) {
     for (uint32_t e = threadIdx.x; e < kMaxExperts; e += kPlaceThreads) total[e] = before[e] = 0;
     __syncthreads();
     wait_prior_grid();
-    // every chunk's counts, 8 experts to a 16-byte piece: a thread sums some chunks' piece
+    // every chunk's counts, 8 experts to a 16-byte piece: a thread sums some chunks' piece.  The
+    // loads of the first are on their way while the chunk's assignments are ranked.
     const uint32_t pieces = a.row / 8, parts = kPlaceThreads / pieces;
-    if (threadIdx.x < parts * pieces) {
-        const uint32_t piece = threadIdx.x % pieces;
+    const uint32_t piece = threadIdx.x % pieces, part = threadIdx.x / pieces;
+    const uint16_t* counts = a.counts + 8 * piece;
+    constexpr uint32_t kEarly = 8;
+    uint4 early[kEarly];
+#pragma unroll
+    for (uint32_t i = 0; i < kEarly; i++) {
+        const uint32_t c = part + i * parts;
+        early[i] = part < parts && c < a.chunks ? *reinterpret_cast<const uint4*>(counts + (uint64_t)c * a.row) : make_uint4(0, 0, 0, 0);
+    }
+    const uint32_t first = blockIdx.x * a.chunk, last = min(a.tokens, first + a.chunk);
+    Ranking ranking(a, first * a.topk, (last - first) * a.topk);
+    ranking.count(warp_base);
+    if (part < parts) {
         uint32_t all[8] = {}, prior[8] = {};
-#pragma unroll 8
-        for (uint32_t c = threadIdx.x / pieces; c < a.chunks; c += parts) {
-            const uint4 v = *reinterpret_cast<const uint4*>(a.counts + (uint64_t)c * a.row + 8 * piece);
+        auto add = [&](const uint4& v, uint32_t c) {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w}, mine = c < blockIdx.x ? 0xffffffffu : 0u;
 #pragma unroll
             for (int j = 0; j < 8; j++) {
@@ -431,7 +567,12 @@ __global__ void __launch_bounds__(kPlaceThreads) k_place(const RouteArgs a) {
                 all[j] += n;
                 prior[j] += n & mine;
             }
-        }
+        };
+#pragma unroll
+        for (uint32_t i = 0; i < kEarly; i++) add(early[i], part + i * parts);
+#pragma unroll 4
+        for (uint32_t c = part + kEarly * parts; c < a.chunks; c += parts)
+            add(*reinterpret_cast<const uint4*>(counts + (uint64_t)c * a.row), c);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             if (all[j]) atomicAdd(total + 8 * piece + j, all[j]);
@@ -444,8 +585,7 @@ __global__ void __launch_bounds__(kPlaceThreads) k_place(const RouteArgs a) {
         for (uint32_t e = threadIdx.x; e <= a.experts; e += kPlaceThreads) a.offsets[e] = (int32_t)offset[e];
     for (uint32_t e = threadIdx.x; e < a.experts; e += kPlaceThreads) before[e] += offset[e];
     __syncthreads();
-    const uint32_t first = blockIdx.x * a.chunk, last = min(a.tokens, first + a.chunk);
-    place_chunk(a, first * a.topk, (last - first) * a.topk, before, warp_base);
+    ranking.place(before, warp_base);
     clear_unused(a, offset[a.experts], blockIdx.x * kPlaceThreads + threadIdx.x, gridDim.x * kPlaceThreads);
 }
 
@@ -462,7 +602,7 @@ cudaError_t launch(const RouteArgs& a, size_t smem, cudaStream_t s) {
     static bool set[5][64] = {};
     auto go = [&](auto* k, bool* attr_set) {
         const cudaError_t e = allow_smem(k, kPlaceWarps * kMaxExperts * sizeof(uint16_t), attr_set);
-        return e != cudaSuccess ? e : launch_programmatic(k, grid, route_threads<MODE>(), smem, s, a);
+        return e != cudaSuccess ? e : launch_programmatic(k, grid, kRouteThreads, smem, s, a);
     };
     if (a.experts <= 32) return go(k_route<1, MODE>, set[0]);
     if (a.experts <= 64) return go(k_route<2, MODE>, set[1]);

@@ -234,7 +234,9 @@ def check(y, x, sx, w, sw, offsets, rows, exact, fill=-7.0):
 
 DENSE = [(1, 128, 128), (1, 1, 16), (1, 4096, 1024), (16, 256, 512), (17, 130, 640), (33, 384, 128), (100, 200, 1000),
          (129, 128, 2048), (240, 100, 500), (241, 256, 256), (500, 700, 300), (1000, 1024, 1100), (3, 513, 4096),
-         (32, 128, 8192), (7, 64, 1)]
+         (32, 128, 8192), (7, 64, 1),
+         # K split over a cluster of 2, 4 and 8; pairs of 240 and of 256 tokens
+         (5, 5000, 1000), (9, 1000, 1300), (1, 1030, 2100), (70, 600, 1500), (480, 300, 260), (512, 600, 700), (1025, 300, 384)]
 
 
 @pytest.mark.parametrize("tokens,rows,cols", DENSE)
@@ -322,21 +324,22 @@ def test_gemm_nan_and_the_extreme_scales(plan):
 
 def test_gemm_bad_offsets_set_the_status_and_stay_inside(plan):
     x, sx, w, sw = grid_case(50, 128, 128, 3, 1)
-    for offsets in ([0, 20, 10, 50], [0, 20, 40, 51], [-1, 20, 30, 50]):
+    for offsets in ([0, 20, 10, 50], [0, 20, 40, 51], [-1, 20, 30, 50], [0, 50, 0, 50], [50, 0, 50, 0]):
         product(plan, x, sx, w, sw, 128, 128, offsets, status=dfx.DFX_STATUS_INDEX)
     y = product(plan, x, sx, w, sw, 128, 128, [0, 20, 30, 50])
     check(y, x, sx, w, sw, [0, 20, 30, 50], 128, exact=True)
 
 
-def test_gemm_wait_that_runs_out_is_reported(plan):
-    """A tile copy that is left out: the status says so, and the next call is sound."""
-    x, sx, w, sw = grid_case(20, 256, 512, 1, 3)
+@pytest.mark.parametrize("tokens,rows,cols", [(20, 256, 512), (1, 128, 100), (100, 2000, 128), (300, 512, 640), (512, 300, 300)])
+def test_gemm_wait_that_runs_out_is_reported(plan, tokens, rows, cols):
+    """Tile copies that are left out: the status says so, and the next call is sound."""
+    x, sx, w, sw = grid_case(tokens, rows, cols, 1, 3)
     dfx.dfx_debug_inject(dfx.DFX_INJECT_SKIP_TILE_COPY)
     try:
-        product(plan, x, sx, w, sw, 256, 512, status=dfx.DFX_STATUS_TIMEOUT)
+        product(plan, x, sx, w, sw, rows, cols, status=dfx.DFX_STATUS_TIMEOUT)
     finally:
         dfx.dfx_debug_inject(0)
-    check(product(plan, x, sx, w, sw, 256, 512), x, sx, w, sw, None, 256, exact=True)
+    check(product(plan, x, sx, w, sw, rows, cols), x, sx, w, sw, None, rows, exact=True)
 
 
 def test_nothing_to_do(plan):
