@@ -37,7 +37,7 @@ struct RouteArgs {
 struct QuantizeArgs {
     const void* x;
     uint64_t ld_x;          // elements between rows of x
-    uint64_t x_rows;
+    uint64_t x_rows, shifted_rows;
     const int32_t* index;   // row of x of each row of q, or NULL
     uint64_t rows, cols;
     uint8_t* q;

@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kQuantThreads, kQuantCtas) k_quantize_rows(con
     uint8_t *out = a.q + row * a.ld_q, *out_s = a.scales + row * a.ld_s;
     const unsigned mask = ((1u << kRowLanes) - 1u) << (kRowLanes * part);
     constexpr int P = SWIGLU ? 2 : 1;
-    Eight<T> p[VEC ? kUnits : 1][2][P];
-    if constexpr (VEC) {
+    Eight<T> p[kUnits][2][P];
+    auto load = [&](auto how) {
 #pragma unroll
         for (uint32_t i = 0; i < kUnits; i++)
 #pragma unroll
@@ -206,11 +206,14 @@ __global__ void __launch_bounds__(kQuantThreads, kQuantCtas) k_quantize_rows(con
                 const uint32_t c = (b0 + kRowBlocks * i) * kScaleBlock + 16 * q + 8 * h;
 #pragma unroll
                 for (int j = 0; j < P; j++) {
-                    if (c < cols) p[i][h][j].load(x + j * cols + c);
+                    if (c < cols) how(p[i][h][j], x + j * cols + c, min(8u, cols - c));
                     else p[i][h][j].zero();
                 }
             }
-    }
+    };
+    if constexpr (VEC) load([](Eight<T>& e, const T* s, uint32_t) { e.load(s); });
+    else if ((uint64_t)from < a.shifted_rows) load([](Eight<T>& e, const T* s, uint32_t n) { e.load_shifted(s, n); });
+    else load([](Eight<T>& e, const T* s, uint32_t n) { e.load_each(s, n); });  // the last row or rows
 #pragma unroll
     for (uint32_t i = 0; i < kUnits; i++) {
         const uint32_t b = b0 + kRowBlocks * i, c0 = b * kScaleBlock + 16 * q;
@@ -219,16 +222,12 @@ __global__ void __launch_bounds__(kQuantThreads, kQuantCtas) k_quantize_rows(con
         float m = 0.0f;
 #pragma unroll
         for (uint32_t h = 0; h < 2; h++) {
-            const uint32_t nh = n > 8 * h ? min(8u, n - 8 * h) : 0, c = c0 + 8 * h;
             float g[8], u[8];
-            if constexpr (VEC) {
-                p[i][h][0].get(SWIGLU ? g : v[h]);
-                if constexpr (SWIGLU) p[i][h][1].get(u);
-            } else {
-                load_some(x + c, nh, SWIGLU ? g : v[h]);
-                if constexpr (SWIGLU) load_some(x + cols + c, nh, u);
+            p[i][h][0].get(SWIGLU ? g : v[h]);
+            if constexpr (SWIGLU) {
+                p[i][h][1].get(u);
+                swiglu(g, u, v[h]);
             }
-            if constexpr (SWIGLU) swiglu(g, u, v[h]);
             m = magnitude(v[h], m);
         }
         m = block_max(mask, m);
@@ -264,13 +263,15 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? kQuantCtas : 2
     const uint32_t n = c < a.cols ? (uint32_t)min((uint64_t)8, a.cols - c) : 0;
     const uint64_t first = rb * kScaleBlock + r0;
     const T* x = (const T*)a.x + first * a.ld_x + c;
+    const bool shifted = (rb + 1) * kScaleBlock <= a.shifted_rows;
     // the block stays in registers as it was loaded
     Eight<T> p[kTallRows];
 #pragma unroll
     for (uint32_t i = 0; i < kTallRows; i++) {
         if (first + 16 * i >= a.rows || n == 0) p[i].zero();
         else if constexpr (VEC) p[i].load(x + 16 * i * a.ld_x);
-        else p[i].load_some(x + 16 * i * a.ld_x, n);
+        else if (shifted) p[i].load_shifted(x + 16 * i * a.ld_x, n);
+        else p[i].load_each(x + 16 * i * a.ld_x, n);
     }
     auto block_of = [&](float m) {
         m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));  // magnitudes: bits in order
@@ -310,7 +311,8 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? kQuantCtas : 2
 }
 
 template <class T>
-cudaError_t launch(const QuantizeArgs& a, cudaStream_t s) {
+cudaError_t launch(QuantizeArgs a, cudaStream_t s) {
+    a.shifted_rows = shifted_rows(a.x_rows, a.ld_x, sizeof(T));
     // 16-byte pieces when every row (and a row's values behind its gates) starts on one and a
     // row holds a whole number of eights
     const bool vec = a.cols % 8 == 0 && a.ld_x * sizeof(T) % 16 == 0;

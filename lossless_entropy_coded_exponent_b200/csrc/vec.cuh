@@ -1,6 +1,7 @@
-// vec.cuh -- eight neighbouring BF16 or FP32 values of a row as FP32, loaded and stored in
-// 16-byte pieces where the row's alignment allows it and one by one where it does not.  Plain
-// loads: the kernel before, in whose last moments these kernels start, may have written them.
+// vec.cuh -- eight neighbouring BF16 or FP32 values of a row, loaded in 16-byte pieces: the row's
+// own where they are aligned, else the aligned pieces that hold the values, shifted together (a row
+// of an odd length starts anywhere).  Plain loads: the kernel before, in whose last moments these
+// kernels start, may have written the values.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -18,6 +19,15 @@ __device__ __forceinline__ void unpack_bf16(uint32_t w, float& lo, float& hi) {
     hi = __uint_as_float(w & 0xffff0000u);
 }
 
+// v[i] = v[i + by], by 0 .. 3; the last ones are of no use then
+template <int N>
+__device__ __forceinline__ void shift_words(uint32_t (&v)[N], uint32_t by) {
+#pragma unroll
+    for (int i = 0; i + 2 < N; i++) v[i] = by & 2 ? v[i + 2] : v[i];
+#pragma unroll
+    for (int i = 0; i + 1 < N; i++) v[i] = by & 1 ? v[i + 1] : v[i];
+}
+
 // The 16-byte pieces of eight values, as they are loaded: kept apart from their conversion
 // so that a thread can have several loads in flight.
 template <class T>
@@ -33,8 +43,21 @@ struct Eight<__nv_bfloat16> {
         unpack_bf16(p.z, v[4], v[5]);
         unpack_bf16(p.w, v[6], v[7]);
     }
-    // n (0 .. 8) values one by one, the others zero
-    __device__ __forceinline__ void load_some(const __nv_bfloat16* s, uint32_t n) {
+    // The first n (0 .. 8) values at s, the others zero: shifted together from the aligned pieces they
+    // are in, of which up to kShiftedSpan bytes from s on are read ...
+    __device__ __forceinline__ void load_shifted(const __nv_bfloat16* s, uint32_t n) {
+        const uint32_t off = (uint32_t)(uintptr_t)s & 15u;
+        const uint4* q = reinterpret_cast<const uint4*>((uintptr_t)s - off);
+        const uint4 lo = q[0], hi = q[1];
+        uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        shift_words(v, off >> 2);
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = __funnelshift_r(v[i], v[i + 1], 8 * (off & 3u));
+        auto keep = [&](uint32_t w, uint32_t i) { return n >= i + 2 ? w : n > i ? w & 0xffffu : 0u; };
+        p = make_uint4(keep(v[0], 0), keep(v[1], 2), keep(v[2], 4), keep(v[3], 6));
+    }
+    // ... or one by one
+    __device__ __forceinline__ void load_each(const __nv_bfloat16* s, uint32_t n) {
         const uint16_t* h = reinterpret_cast<const uint16_t*>(s);
         uint32_t w[8];
 #pragma unroll
@@ -54,7 +77,23 @@ struct Eight<float> {
         v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
         v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
     }
-    __device__ __forceinline__ void load_some(const float* s, uint32_t n) {
+    __device__ __forceinline__ void load_shifted(const float* s, uint32_t n) {
+        const uint32_t off = (uint32_t)(uintptr_t)s & 15u;
+        const uint4* at = reinterpret_cast<const uint4*>((uintptr_t)s - off);
+        uint32_t w[12];
+#pragma unroll
+        for (int i = 0; i < 3; i++) {
+            const uint4 four = at[i];
+            w[4 * i] = four.x, w[4 * i + 1] = four.y, w[4 * i + 2] = four.z, w[4 * i + 3] = four.w;
+        }
+        shift_words(w, off >> 2);
+        float v[8];
+#pragma unroll
+        for (uint32_t i = 0; i < 8; i++) v[i] = i < n ? __uint_as_float(w[i]) : 0.0f;
+        p = make_float4(v[0], v[1], v[2], v[3]);
+        q = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    __device__ __forceinline__ void load_each(const float* s, uint32_t n) {
         float v[8];
 #pragma unroll
         for (uint32_t i = 0; i < 8; i++) v[i] = i < n ? s[i] : 0.0f;
@@ -63,11 +102,12 @@ struct Eight<float> {
     }
 };
 
-// n (0 .. 8) values at s one by one, the others zero
-template <class T>
-__device__ __forceinline__ void load_some(const T* s, uint32_t n, float (&v)[8]) {
-#pragma unroll
-    for (uint32_t i = 0; i < 8; i++) v[i] = i < n ? as_f32(s[i]) : 0.0f;
+constexpr uint64_t kShiftedSpan = 48;
+// Rows of a matrix (of `rows`, ld elements apart) from which load_shifted of any value before `cols`
+// stays inside the matrix: kShiftedSpan bytes behind the row there are still rows.
+inline uint64_t shifted_rows(uint64_t rows, uint64_t ld, uint64_t element_bytes) {
+    const uint64_t last = (kShiftedSpan + ld * element_bytes - 1) / (ld * element_bytes);
+    return rows > last ? rows - last : 0;
 }
 
 // FP32 to BF16 rounds to nearest, ties to even
