@@ -387,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         start[0] = 0;
         start[1] = (a.g.tokens + S::kCap - 1) / S::kCap * a.row_units;
     }
+    __syncwarp();
     tc_fence_before();
     sync_ctas(ctas > 1);
     tc_fence_after();
@@ -606,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     if (err) atomicOr(a.g.status, err);
+    __syncwarp();
     tc_fence_before();
     sync_ctas(ctas > 1);
     if (warp == 1) {

@@ -5,9 +5,10 @@
 // a token if its logit is above -inf and not NaN (and its bias, where there is one).  The
 // choice goes by s + bias among open experts, of the best groups only where there are groups;
 // the weights are the scores without the bias.  Without a bias the order of s is the order of
-// l, so the logits themselves are compared.  Where s + bias or a sum of scores decides, it is
-// formed in FP64: two experts whose choices are nearer than FP32's rounding would otherwise
-// come in an order that hangs on how a sum was formed.  Ties go to the lowest index.
+// l, so the logits themselves are compared.  Where s + bias or a sum of scores decides, the order is
+// that of FP64: two experts whose choices are nearer than FP32's rounding would otherwise come in
+// an order that hangs on how a sum was formed.  The picks are made in FP32, and again in FP64 where
+// two that decide are too near (quick_picks).  Ties go to the lowest index.
 //
 // k_route: a warp per token, a few tokens after one another.  Lane i holds the experts
 // i * KPL .. i * KPL + KPL - 1 as unsigned integers in the order of their values (0: not open), so
@@ -20,6 +21,10 @@
 // then ranks its chunk's assignments: within 32 of them by a match of equal experts, across
 // warps by counts, always in the order of the tokens, so the result does not depend on timing.
 // Up to kOneChunk tokens one CTA does both in one launch.
+//
+// Bound by instructions and their latency, not by memory: 32749 tokens over 128 experts, 8 each, in
+// 25 us (2 us for their bytes), of which k_route takes 14.6; 4096 over 256 in 8 groups with a bias in
+// 20 (13.3; 29 with every choice in FP64).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
