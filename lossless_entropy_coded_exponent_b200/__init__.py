@@ -462,6 +462,18 @@ def _ld(x) -> int:
     return max(x.stride(0), x.shape[1])
 
 
+def _whole_fp8(f: Fp8, what: str):
+    """Refuses an Fp8 whose tensors are not laid out as its rows and columns say."""
+    import torch
+
+    rows, blocks = f.values.shape[-2], -(-f.cols // 128)
+    if f.values.dtype != torch.uint8 or f.scales.dtype != torch.uint8:
+        raise TypeError(f"{what}: values and scales are uint8 tensors")
+    if not f.values.is_contiguous() or not f.scales.is_contiguous() or f.values.shape[:-2] != f.scales.shape[:-2] \
+            or f.scales.shape[-2] != -(-rows // f.block_rows) or f.values.shape[-1] < f.cols or f.scales.shape[-1] < blocks:
+        raise ValueError(f"{what}: values and scales are contiguous, with a row of scales for {f.block_rows} of values")
+
+
 def _same_device(what: str, *tensors):
     if len({t.device for t in tensors if t is not None}) > 1:
         raise ValueError(f"{what}: tensors on different devices")
@@ -537,11 +549,14 @@ def gemm_fp8(x: Fp8, w: Fp8, offsets=None, dtype=None, out=None, plan: Plan | No
         raise ValueError("gemm_fp8: x in blocks of 1 x 128, w in blocks of 128 x 128")
     if x.cols != w.cols:
         raise ValueError(f"gemm_fp8: rows of {x.cols} and of {w.cols} values")
+    _whole_fp8(x, "gemm_fp8")
+    _whole_fp8(w, "gemm_fp8")
     experts = w.values.shape[0] if w.values.dim() == 3 else 1
     if offsets is not None and (offsets.dtype != torch.int32 or offsets.shape != (experts + 1,) or not offsets.is_contiguous()):
         raise ValueError("gemm_fp8: offsets is an int32 vector of one more than the experts")
     _same_device("gemm_fp8", x.values, x.scales, w.values, w.scales, offsets, out)
-    if out is not None and (out.dim() != 2 or out.stride(1) != 1 or out.shape != (x.values.shape[0], w.values.shape[-2])
+    if out is not None and (out.dim() != 2 or out.stride(1) != 1 or (out.shape[0] > 1 and out.stride(0) < out.shape[1])
+                            or out.shape != (x.values.shape[0], w.values.shape[-2])
                             or (dtype is not None and out.dtype != dtype)):
         raise ValueError("gemm_fp8: out is a [tokens, rows] matrix with neighbouring elements")
     dtype = out.dtype if out is not None else dtype or torch.bfloat16

@@ -31,8 +31,8 @@
 //   2     lays out the scale bytes in shared memory: byte j of word (32 i + l) of a 512-byte
 //         tile is the scale of row 32 i + l and block 4 g + j (row l's four words are
 //         neighbours), which tcgen05.cp spreads over the lanes;
-//   4-7   read the accumulator (lane = row of W) and write Y, while the next unit's MMAs run
-//         into the other accumulator.
+//   4-7, 4-11 for up to 128 tokens: read the accumulator (lane = row of W) and write Y, while the
+//         next unit's MMAs run into the other accumulator.
 // Every wait is bounded: one that runs out sets DFX_STATUS_TIMEOUT, the CTA's warps leave their
 // loops, and the copies and MMAs in flight are waited for before the tensor memory is freed.
 #include <cuda.h>
@@ -50,7 +50,6 @@
 namespace dfx {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr uint32_t kTileRows = 128;                       // rows of W per tile: the MMA's M
 constexpr uint32_t kTileK = 128;                          // values of K per stage: one scale block
 constexpr uint32_t kABytes = kTileRows * kTileK;          // 16 KiB
@@ -67,6 +66,11 @@ struct Shape {
     static constexpr uint32_t kCap = CAP;
     static constexpr bool kPair = PAIR;
     static constexpr uint32_t kCtas = PAIR ? 2 : 1;
+    // Warps that write Y, from warp 4 on.  Eight (two to a quarter of the lanes) where 128 tokens
+    // are written when nothing is left to multiply: 123 tokens through 5619 x 4007 in 14.4 us, with
+    // four 16.6.  Beside a pair's MMAs eight are in the way: 8192 tokens take 3 % longer.
+    static constexpr uint32_t kEpilogueWarps = CAP == 128 ? 8 : 4, kColumnStep = 4 * kEpilogueWarps;
+    static constexpr int kThreads = 32 * (4 + kEpilogueWarps);
     static constexpr uint32_t kHeld = CAP / kCtas;                     // tokens in one CTA's memory
     static constexpr uint32_t kUnitRows = kCtas * kTileRows;
     static constexpr uint32_t kBox = CAP == 256 ? 64 : PAIR ? 40 : 32;
@@ -269,15 +273,16 @@ struct ScaleChunk {
     }
 };
 
-// A unit's columns (tokens) of this lane's row of W to Y (y: the first token's element of the row)
-template <class T>
-__device__ __forceinline__ void store_columns(T* y, uint64_t ld, uint32_t taddr, const Unit& w, bool inside) {
+// A unit's columns (tokens) of this lane's row of W to Y (y: the first token's element of the row),
+// 16 from c0 on and from every kColumnStep behind it
+template <class S, class T>
+__device__ __forceinline__ void store_columns(T* y, uint64_t ld, uint32_t taddr, uint32_t c0, const Unit& w, bool inside) {
 #pragma unroll 1
-    for (uint32_t c = 0; c < w.columns; c += 16, y += 16 * ld) {
+    for (uint32_t c = c0; c < w.columns; c += S::kColumnStep) {
         uint32_t v[16];
         tmem_ld16(taddr + c, v);
         if (inside) {
-            T* d = y;
+            T* d = y + c * ld;
 #pragma unroll
             for (uint32_t j = 0; j < 16; j++, d += ld)
                 if (c + j < w.n) store_one(d, __uint_as_float(v[j]));
@@ -309,7 +314,7 @@ __device__ __forceinline__ void store_four(__nv_bfloat16* d, bool whole, const f
 }
 
 template <class S>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(S::kThreads, 1)
     k_gemm_fp8(const __grid_constant__ KernelArgs a, const __grid_constant__ CUtensorMap map_x,
                const __grid_constant__ CUtensorMap map_w) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -346,15 +351,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = 0; i < S::kStages; i++) mbar_init_count(&bar_full[i], 1), mbar_init_count(&bar_free[i], 1);
         for (uint32_t i = 0; i < S::kSlots; i++)
             mbar_init_count(&bar_scale[i], S::kCtas), mbar_init_count(&bar_scale_free[i], 1);
-        for (uint32_t i = 0; i < 2; i++) mbar_init_count(&bar_acc[i], 1), mbar_init_count(&bar_acc_free[i], 4 * S::kCtas);
-        mbar_init_count(&bar_part, 4 * ctas);
+        for (uint32_t i = 0; i < 2; i++) mbar_init_count(&bar_acc[i], 1), mbar_init_count(&bar_acc_free[i], S::kEpilogueWarps * S::kCtas);
+        mbar_init_count(&bar_part, S::kEpilogueWarps * ctas);
         fence_mbar_init();
     }
     wait_prior_grid();
     uint32_t err = 0;
     // the experts' rows, clamped to X, and their units
     if (a.g.offsets) {
-        for (uint32_t e = threadIdx.x; e < a.g.experts; e += kThreads) {
+        for (uint32_t e = threadIdx.x; e < a.g.experts; e += S::kThreads) {
             const int32_t o0 = a.g.offsets[e], o1 = a.g.offsets[e + 1];
             const uint32_t lo = (uint32_t)min(max(o0, 0), (int32_t)a.g.tokens);
             const uint32_t hi = (uint32_t)min(max(o1, (int32_t)lo), (int32_t)a.g.tokens);
@@ -542,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ epilogue
-        const uint32_t quarter = warp - 4;  // tensor-memory lanes 32 quarter .. + 31
+        // tensor-memory lanes 32 quarter .. + 31; of eight warps every second 16 columns
+        const uint32_t quarter = warp % 4, c0 = (warp - 4) / 4 * 16;
         uint32_t acc = 0, acc_ph = 0;
         for (uint32_t u = first; u < units; u += step) {
             const Unit w = walk.at(u);
@@ -551,13 +557,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t in_tile = 32 * quarter + lane, row = (w.row_unit * S::kCtas + rank) * kTileRows + in_tile;
             const uint32_t taddr = tmem + acc * S::kCap + ((32 * quarter) << 16);
             if (P || a.split == 1) {
-                if (a.g.y_f32) store_columns((float*)a.g.y + (uint64_t)w.first * a.g.ld_y + row, a.g.ld_y, taddr, w, row < a.g.rows);
-                else store_columns((__nv_bfloat16*)a.g.y + (uint64_t)w.first * a.g.ld_y + row, a.g.ld_y, taddr, w, row < a.g.rows);
+                if (a.g.y_f32) store_columns<S>((float*)a.g.y + (uint64_t)w.first * a.g.ld_y + row, a.g.ld_y, taddr, c0, w, row < a.g.rows);
+                else store_columns<S>((__nv_bfloat16*)a.g.y + (uint64_t)w.first * a.g.ld_y + row, a.g.ld_y, taddr, c0, w, row < a.g.rows);
             } else {
                 // Every CTA lays its sums out in its tile memory, which its MMAs have read, as
                 // [token][row].  Then every CTA of the cluster adds up its share of them, four rows
                 // at a time, in the order of K's parts.
-                for (uint32_t c = 0; c < w.n; c += 16) {
+                for (uint32_t c = c0; c < w.n; c += S::kColumnStep) {
                     uint32_t v[16];
                     tmem_ld16(taddr + c, v);
 #pragma unroll
@@ -576,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr uint32_t kFours = kTileRows / 4;
                 const uint32_t share = (w.n * kFours + a.split - 1) / a.split;
                 const uint32_t last = min(w.n * kFours, (in_cluster + 1) * share);
-                for (uint32_t i = in_cluster * share + in_tile; i < last; i += kTileRows) {
+                for (uint32_t i = in_cluster * share + threadIdx.x - 128; i < last; i += 32 * S::kEpilogueWarps) {
                     const uint32_t t = i / kFours, r = w.row_unit * kTileRows + 4 * (i % kFours);
                     if (r >= a.g.rows) continue;
                     float4 q[kMaxSplit];
@@ -673,7 +679,7 @@ cudaError_t cluster_slots(uint32_t split, int sms, uint64_t* slots) {
     if (known[dev][split] == 0) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(ctas);
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(S::kThreads);
         cfg.dynamicSmemBytes = most;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -707,7 +713,7 @@ cudaError_t launch(const GemmFp8Args& g, uint32_t split, uint64_t slots, cudaStr
     const uint32_t ctas = S::kCtas * split;
     const uint64_t units = most_runs<S>(g) * a.row_units;
     const int grid = (int)((units < slots || split > 1 ? units : slots) * ctas);
-    return launch_clusters(k_gemm_fp8<S>, grid, ctas, kThreads, S::kSmem + (3 * g.experts + 1) * sizeof(uint32_t), s, a, mx,
+    return launch_clusters(k_gemm_fp8<S>, grid, ctas, S::kThreads, S::kSmem + (3 * g.experts + 1) * sizeof(uint32_t), s, a, mx,
                            mw);
 }
 

@@ -140,6 +140,32 @@ struct KeyOf<kBf16Logits> { using type = uint32_t; };
 __device__ __forceinline__ void logit_key(float x, uint32_t e, uint32_t& key) { key = (ordered(x) & 0xffff0000u) | (0xffffu - e); }
 __device__ __forceinline__ void logit_key(float x, uint32_t e, uint64_t& key) { key = (uint64_t)ordered(x) << 32 | (0xffffu - e); }
 
+// The best two keys of the experts of a group: those whose place from `at` on (of this lane's first
+// expert, from the group's first) is below `per`.
+template <int KPL, class Key>
+__device__ __forceinline__ void best_of_group(const Key (&key)[KPL], uint32_t at, uint32_t per, Key& best, Key& second) {
+    Key m = 0, m2 = 0;  // the lane's own
+#pragma unroll
+    for (int j = 0; j < KPL; j++) {
+        const Key k = at + j < per ? key[j] : 0;
+        m2 = max(m2, min(m, k));
+        m = max(m, k);
+    }
+    best = warp_max(m);
+    const uint32_t first = __ffs((int)__ballot_sync(kFull, m == best)) - 1;
+    second = warp_max((threadIdx.x & 31) == first ? m2 : m);
+}
+// keys outside the groups of the mask `kept` become 0
+template <int KPL, class Key>
+__device__ __forceinline__ void drop_groups(const RouteArgs& a, Key (&key)[KPL], uint32_t e0, uint32_t per, uint32_t kept) {
+    for (uint32_t g = 0; g < a.groups; g++) {
+        if ((kept >> g) & 1u) continue;
+#pragma unroll
+        for (int j = 0; j < KPL; j++)
+            if (e0 + j - g * per < per) key[j] = 0;
+    }
+}
+
 // One token by one warp: the keys of its experts, those outside its best groups 0.
 // top, denominator: what its softmax needs.
 template <int KPL, int MODE, class Key>
@@ -217,20 +243,9 @@ __device__ __forceinline__ void token_keys(const RouteArgs& a, const float (&x)[
         }
         mine = __shfl_sync(kFull, score_of(best, second), lane * lanes);  // wraps for lanes past the groups
     } else {
-        uint32_t group[KPL];
-#pragma unroll
-        for (int j = 0; j < KPL; j++) group[j] = (e0 + j) / per;
         for (uint32_t g = 0; g < a.groups; g++) {
-            Key m = 0, m2 = 0;  // the lane's best two of the group
-#pragma unroll
-            for (int j = 0; j < KPL; j++) {
-                const Key k = group[j] == g ? key[j] : 0;
-                m2 = max(m2, min(m, k));
-                m = max(m, k);
-            }
-            const Key best = warp_max(m);
-            const uint32_t first = __ffs((int)__ballot_sync(kFull, m == best)) - 1;
-            const Key second = warp_max(lane == first ? m2 : m);
+            Key best, second;
+            best_of_group<KPL>(key, e0 - g * per, per, best, second);
             if (lane == g) mine = score_of(best, second);
         }
     }
@@ -240,9 +255,7 @@ __device__ __forceinline__ void token_keys(const RouteArgs& a, const float (&x)[
         above += other > mine || (other == mine && g < lane);
     }
     const uint32_t kept = __ballot_sync(kFull, lane < a.groups && above < a.top_groups);
-#pragma unroll
-    for (int j = 0; j < KPL; j++)
-        if (e0 + j < a.experts && !((kept >> ((e0 + j) / per)) & 1u)) key[j] = 0;
+    drop_groups<KPL>(a, key, e0, per, kept);
 }
 
 __device__ __forceinline__ float value_of(uint32_t key) {
@@ -288,20 +301,30 @@ __device__ __forceinline__ bool quick_picks(const RouteArgs& a, const float (&x)
     bool sure = true;
     if (a.groups > 1) {
         const uint32_t per = a.experts / a.groups, lanes = per / KPL;
-        if (per % KPL != 0 || (lanes & (lanes - 1)) != 0) return false;  // a group is no run of whole lanes
-        uint32_t best = 0, second = 0;
+        auto score_of = [&](uint32_t best, uint32_t second) {
+            return a.group_best == 2 && second != 0 ? ordered(value_of(best) + value_of(second)) : best;
+        };
+        uint32_t mine = 0;
+        if (per % KPL == 0 && (lanes & (lanes - 1)) == 0) {
+            uint32_t best = 0, second = 0;
 #pragma unroll
-        for (int j = 0; j < KPL; j++) {
-            second = max(second, min(best, key[j]));
-            best = max(best, key[j]);
+            for (int j = 0; j < KPL; j++) {
+                second = max(second, min(best, key[j]));
+                best = max(best, key[j]);
+            }
+            for (uint32_t d = 1; d < lanes; d <<= 1) {
+                const uint32_t other = __shfl_xor_sync(kFull, best, d), other2 = __shfl_xor_sync(kFull, second, d);
+                second = max(min(best, other), max(second, other2));
+                best = max(best, other);
+            }
+            mine = __shfl_sync(kFull, score_of(best, second), lane * lanes);
+        } else {
+            for (uint32_t g = 0; g < a.groups; g++) {
+                uint32_t best, second;
+                best_of_group<KPL>(key, e0 - g * per, per, best, second);
+                if (lane == g) mine = score_of(best, second);
+            }
         }
-        for (uint32_t d = 1; d < lanes; d <<= 1) {
-            const uint32_t other = __shfl_xor_sync(kFull, best, d), other2 = __shfl_xor_sync(kFull, second, d);
-            second = max(min(best, other), max(second, other2));
-            best = max(best, other);
-        }
-        const uint32_t score = a.group_best == 2 && second != 0 ? ordered(value_of(best) + value_of(second)) : best;
-        const uint32_t mine = __shfl_sync(kFull, score, lane * lanes);
         uint32_t above = 0;
         for (uint32_t g = 0; g < a.groups; g++) {
             const uint32_t other = __shfl_sync(kFull, mine, g);
@@ -315,10 +338,7 @@ __device__ __forceinline__ bool quick_picks(const RouteArgs& a, const float (&x)
             const float l = value_of(low), h = value_of(high);
             sure = l - h > 2.0f * tolerance * (1.0f + fabsf(h));
         }
-        if (!((kept >> (lane / lanes)) & 1u)) {
-#pragma unroll
-            for (int j = 0; j < KPL; j++) key[j] = 0;
-        }
+        drop_groups<KPL>(a, key, e0, per, kept);
     }
     float last = 0.0f;
     for (uint32_t k = 0; k <= a.topk; k++) {  // one more than is picked: the last must stand clear too

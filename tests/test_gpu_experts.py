@@ -162,6 +162,12 @@ def test_helpers_take_views_and_refuse_the_rest():
     with pytest.raises(ValueError):
         dfx.gemm_fp8(q, dfx.quantize_fp8(torch.randn(64, 256, device="cuda"), block_rows=128))
     with pytest.raises(ValueError):
+        dfx.gemm_fp8(q, w, out=out[:1, :64].expand(40, 64))  # rows on top of one another
+    with pytest.raises(ValueError):
+        dfx.gemm_fp8(q._replace(scales=q.scales[:39]), w)
+    with pytest.raises(ValueError):
+        dfx.gemm_fp8(q, w._replace(values=w.values[:, :256]))
+    with pytest.raises(ValueError):
         dfx.quantize_fp8(torch.zeros(4, 4))                 # not on a GPU
     with pytest.raises(TypeError):
         dfx.quantize_fp8(torch.zeros(4, 4, device="cuda", dtype=torch.float16))

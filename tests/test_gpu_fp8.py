@@ -279,6 +279,9 @@ GROUPED = [
     (700, 200, 300, [0, 1, 500, 500, 690]),
     (40, 128, 128, [0] * 41),                           # no expert has a token
     (200, 128, 160, list(range(0, 201))),               # 200 experts of one token each
+    (900, 20, 130, [0] * 500 + list(range(0, 524)) + [880]),  # as many experts as there may be
+    (260, 140, 256, [0, 129, 260]),                     # runs of an expert on both sides of a tile's cap
+    (1500, 300, 256, [0, 700, 1480]),                   # pairs of CTAs
 ]
 
 
