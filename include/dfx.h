@@ -404,8 +404,9 @@ int dfx_quantize_fp8(dfx_plan_t plan, const void *d_x, uint32_t x_type, uint64_t
 
 /* Y = X W^T of 8-bit operands: Y[t, r] = sum over the blocks b of
  * x_scale[t, b] w_scale[r / 128, b] sum over k in b of x[t, k] w[r, k], accumulated in FP32 on
- * the tensor cores (tcgen05.mma takes the scales with the values) in an order of the hardware's
- * choosing, and rounded once, to y_type.
+ * the tensor cores (tcgen05.mma takes the scales with the values; up to 8 tokens and a matrix of up
+ * to 16 MiB: mma.sync, block by block) in an order of the hardware's choosing, and rounded once,
+ * to y_type.
  *   d_x, ld_x, d_x_scales, ld_x_scales: tokens x cols, blocks of 1 x 128.
  *   d_w, ld_w, d_w_scales, ld_w_scales: experts matrices of rows x cols, blocks of 128 x 128, one
  *     behind the other: matrix e starts at row e * rows of d_w, and at row

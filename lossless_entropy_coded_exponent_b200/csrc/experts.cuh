@@ -78,6 +78,9 @@ uint64_t route_workspace_bytes(uint64_t tokens, uint32_t experts);
 cudaError_t launch_route(RouteArgs a, cudaStream_t s);
 cudaError_t launch_quantize_fp8(const QuantizeArgs& a, cudaStream_t s);
 cudaError_t launch_gemm_fp8(const GemmFp8Args& a, int sms, cudaStream_t s);
+constexpr uint32_t kStreamTokens = 8;  // most tokens of launch_stream_fp8
+bool stream_fp8_takes(const GemmFp8Args& a, int sms);
+cudaError_t launch_stream_fp8(const GemmFp8Args& a, int sms, cudaStream_t s);
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s);
 
 }  // namespace dfx

@@ -8,7 +8,8 @@
 // accumulator: no step that takes it out, scales and adds.
 //
 // W's rows are the MMA's M (a tile is 128 rows: one row of scale blocks), tokens its N: 16 to
-// kCap columns, chosen per unit, so one token and thousands run through the same code.  An MMA of
+// kCap columns, chosen per unit, so one token and thousands run through the same code (up to eight
+// tokens and a small matrix leave it to stream_fp8.cu).  An MMA of
 // K = 32 takes some 120 cycles for any N (measured with the copies left out), so a unit costs
 // the cores the same for one token and for 240; with tokens as M and 240 rows of W as N one token
 // would cost half, but the weights of a decoding step streamed 15 to 20 % slower that way.
@@ -762,6 +763,8 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& g, int sms, cudaStream_t s) {
     using Pair = Shape<240, true>;
     using PairLong = Shape<256, true>;  // of one matrix: powers of two of tokens in fewer runs (512 by
                                         // 14336 x 4096: 37 us, against 43)
+    // an injected failure is one of the tiles'
+    if (!g.inject && stream_fp8_takes(g, sms)) return launch_stream_fp8(g, sms, s);
     const uint64_t mean = (g.tokens + g.experts - 1) / g.experts;
     Choice best;
     cudaError_t e = cudaSuccess;

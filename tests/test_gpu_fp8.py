@@ -350,3 +350,51 @@ def test_nothing_to_do(plan):
     dfx.dfx_gemm_fp8(plan, None, 16, None, 4, 5, None, 16, None, 4, 0, 16, 1, None, None, dfx.DFX_F32, 0)
     dfx.dfx_quantize_fp8(plan, None, dfx.DFX_F32, 16, 0, None, 0, 16, 1, 0, None, 16, None, 4)
     assert dfx.dfx_device_status(plan) == 0
+
+
+# One to eight tokens, one matrix: rows spread over the SMs, two rows of scales in a tile, K's last
+# block cut at several places of its 16 bytes, the most rows and blocks of one round of loads and more.
+FEW = [(1, 1, 1), (2, 147, 15), (3, 149, 17), (8, 2500, 31), (5, 2368, 1000), (7, 2369, 300), (8, 500, 8192), (4, 130, 8193),
+       (8, 4096, 4096), (6, 4737, 4100), (1, 18944, 100), (8, 18945, 130), (2, 18945, 128), (1, 7, 5000), (8, 16, 1024)]
+
+
+@pytest.mark.parametrize("tokens,rows,cols", FEW)
+@pytest.mark.parametrize("y_type", [torch.float32, torch.bfloat16])
+def test_gemm_few_tokens_exact_on_integers(plan, tokens, rows, cols, y_type):
+    x, sx, w, sw = grid_case(tokens, rows, cols, 1, rows)
+    y = product(plan, x, sx, w, sw, rows, cols, y_type=y_type, ld_y=rows + 5)
+    check(y, x, sx, w, sw, None, rows, exact=True)
+
+
+@pytest.mark.parametrize("tokens,rows,cols", [(1, 1000, 4096), (8, 700, 2000), (3, 3000, 520)])
+def test_gemm_few_tokens_gaussian(plan, tokens, rows, cols):
+    x, sx, w, sw = gaussian_case(tokens, rows, cols, 1, 6)
+    check(product(plan, x, sx, w, sw, rows, cols), x, sx, w, sw, None, rows, exact=False)
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 7, 8, 9])
+def test_gemm_few_tokens_scales_and_nan(plan, tokens):
+    """Scale bytes of which only the product is in FP32's range, NaN scales, and a NaN value of W and of X."""
+    rows, cols = 300, 640
+    x = torch.ones(tokens, cols).to(torch.float8_e4m3fn)
+    w = torch.ones(1, rows, cols).to(torch.float8_e4m3fn)
+    sx = torch.tensor([[0, 254, 250, 2, 127]], dtype=torch.uint8).repeat(tokens, 1)
+    sw = torch.tensor([[254, 0, 1, 254, 127]], dtype=torch.uint8).repeat(3, 1)[None].contiguous()
+    want = 128 * (1 + 1 + 0.125 + 4 + 1)  # 128 products a block, times 2^(sx + sw - 254)
+    assert torch.all(product(plan, x, sx, w, sw, rows, cols) == want)
+    bad = sw.clone()
+    bad[0, 1, 3] = 255
+    y = product(plan, x, sx, w, bad, rows, cols)
+    assert torch.all(torch.isnan(y[:, 128:256])) and torch.all(y[:, :128] == want) and torch.all(y[:, 256:] == want)
+    bad = sx.clone()
+    bad[tokens - 1, 0] = 255
+    y = product(plan, x, bad, w, sw, rows, cols)
+    assert torch.all(torch.isnan(y[tokens - 1])) and torch.all(y[: tokens - 1] == want)
+    bad = w.clone().view(torch.uint8)
+    bad[0, 200, 639] = 0xFF
+    y = product(plan, x, sx, bad.view(torch.float8_e4m3fn), sw, rows, cols)
+    assert torch.all(torch.isnan(y[:, 200])) and torch.all(y[:, :200] == want) and torch.all(y[:, 201:] == want)
+    bad = x.clone().view(torch.uint8)
+    bad[0, 0] = 0x7F
+    y = product(plan, bad.view(torch.float8_e4m3fn), sx, w, sw, rows, cols)
+    assert torch.all(torch.isnan(y[0])) and torch.all(y[1:] == want)
