@@ -155,9 +155,48 @@ __device__ __forceinline__ void best_of_group(const Key (&key)[KPL], uint32_t at
     const uint32_t first = __ffs((int)__ballot_sync(kFull, m == best)) - 1;
     second = warp_max((threadIdx.x & 31) == first ? m2 : m);
 }
+// Lane g gets the best two keys of group g (0: none; the second only where it counts).
+template <int KPL, class Key>
+__device__ __forceinline__ void best_of_groups(const RouteArgs& a, const Key (&key)[KPL], uint32_t e0, Key& best, Key& second) {
+    const uint32_t lane = threadIdx.x & 31, per = a.experts / a.groups, lanes = per / KPL;
+    best = second = 0;
+    if (per % KPL == 0 && (lanes & (lanes - 1)) == 0) {
+        // a group is `lanes` whole lanes: their best two, then an exchange among them
+#pragma unroll
+        for (int j = 0; j < KPL; j++) {
+            second = max(second, min(best, key[j]));
+            best = max(best, key[j]);
+        }
+        for (uint32_t d = 1; d < lanes; d <<= 1) {
+            const Key other = __shfl_xor_sync(kFull, best, d), other2 = __shfl_xor_sync(kFull, second, d);
+            second = max(min(best, other), max(second, other2));
+            best = max(best, other);
+        }
+        best = __shfl_sync(kFull, best, lane * lanes);  // wraps for lanes past the groups
+        if (a.group_best == 2) second = __shfl_sync(kFull, second, lane * lanes);
+    } else {
+        for (uint32_t g = 0; g < a.groups; g++) {
+            Key b, c;
+            best_of_group<KPL>(key, e0 - g * per, per, b, c);
+            if (lane == g) best = b, second = c;
+        }
+    }
+}
+// The mask of the best top_groups groups by the scores that the first lanes hold.
+template <class Key>
+__device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, Key mine) {
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t above = 0;  // groups that come before lane's
+    for (uint32_t g = 0; g < a.groups; g++) {
+        const Key other = __shfl_sync(kFull, mine, g);
+        above += other > mine || (other == mine && g < lane);
+    }
+    return __ballot_sync(kFull, lane < a.groups && above < a.top_groups);
+}
 // keys outside the groups of the mask `kept` become 0
 template <int KPL, class Key>
-__device__ __forceinline__ void drop_groups(const RouteArgs& a, Key (&key)[KPL], uint32_t e0, uint32_t per, uint32_t kept) {
+__device__ __forceinline__ void drop_groups(const RouteArgs& a, Key (&key)[KPL], uint32_t e0, uint32_t kept) {
+    const uint32_t per = a.experts / a.groups;
     for (uint32_t g = 0; g < a.groups; g++) {
         if ((kept >> g) & 1u) continue;
 #pragma unroll
@@ -171,7 +210,6 @@ __device__ __forceinline__ void drop_groups(const RouteArgs& a, Key (&key)[KPL],
 template <int KPL, int MODE, class Key>
 __device__ __forceinline__ void token_keys(const RouteArgs& a, const float (&x)[KPL], uint32_t e0, Key (&key)[KPL], float& top,
                                            double& denominator) {
-    const uint32_t lane = threadIdx.x & 31;
     constexpr float kNone = -INFINITY;
     top = kNone;
     denominator = 0.0;
@@ -219,43 +257,12 @@ __device__ __forceinline__ void token_keys(const RouteArgs& a, const float (&x)[
     }
 
     if (a.groups <= 1) return;
-    // lane g gets group g's score: its best key, or the sum of its best two choices
-    const uint32_t per = a.experts / a.groups;
-    Key mine = 0;
-    auto score_of = [&](Key best, Key second) {
-        if constexpr (MODE == kChoices)
-            if (a.group_best == 2 && second != 0) return (Key)ordered(value_of(best) + value_of(second));
-        return best;
-    };
-    const uint32_t lanes = per / KPL;
-    if (per % KPL == 0 && (lanes & (lanes - 1)) == 0) {
-        // a group is `lanes` whole lanes: their best two, then an exchange among them
-        Key best = 0, second = 0;
-#pragma unroll
-        for (int j = 0; j < KPL; j++) {
-            second = max(second, min(best, key[j]));
-            best = max(best, key[j]);
-        }
-        for (uint32_t d = 1; d < lanes; d <<= 1) {
-            const Key other = __shfl_xor_sync(kFull, best, d), other2 = __shfl_xor_sync(kFull, second, d);
-            second = max(min(best, other), max(second, other2));
-            best = max(best, other);
-        }
-        mine = __shfl_sync(kFull, score_of(best, second), lane * lanes);  // wraps for lanes past the groups
-    } else {
-        for (uint32_t g = 0; g < a.groups; g++) {
-            Key best, second;
-            best_of_group<KPL>(key, e0 - g * per, per, best, second);
-            if (lane == g) mine = score_of(best, second);
-        }
-    }
-    uint32_t above = 0;  // groups that come before lane's
-    for (uint32_t g = 0; g < a.groups; g++) {
-        const Key other = __shfl_sync(kFull, mine, g);
-        above += other > mine || (other == mine && g < lane);
-    }
-    const uint32_t kept = __ballot_sync(kFull, lane < a.groups && above < a.top_groups);
-    drop_groups<KPL>(a, key, e0, per, kept);
+    // lane g: group g's score, its best key or the sum of its best two choices
+    Key mine, second;
+    best_of_groups<KPL>(a, key, e0, mine, second);
+    if constexpr (MODE == kChoices)
+        if (a.group_best == 2 && second != 0) mine = ordered(value_of(mine) + value_of(second));
+    drop_groups<KPL>(a, key, e0, kept_groups(a, mine));
 }
 
 __device__ __forceinline__ float value_of(uint32_t key) {
@@ -263,11 +270,14 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 }
 
 // The picks of one token whose choices are sums, in FP32: true if no two choices (or groups) that
-// decide are nearer than their rounding.  An error is at most 2^-21 of 1 + |choice| for a sigmoid
-// (exponential 2^-22, sum and quotient 2^-24 each, the bias' sum 2^-24), and 2^-19 for a softmax
-// (up to 21 additions of 2^-24 more), and the key's last bits, given to its place in the lane, are
-// 2^-20 of the choice; a difference is trusted from 2^-18 and 2^-16 on.  Lane first_lane + k gets
-// pick k in id.
+// decide are nearer than their rounding.  The error of a choice c: of its score at most 2^-21 for a
+// sigmoid (exponential 2^-22, sum and quotient 2^-24 each), 2^-19 for a softmax (up to 21 additions of
+// 2^-24 more); 2^-24 |c| from adding the bias; and the key's last bits, given to its place in the lane,
+// (KPL - 1) 2^-23 |c|, which is below 2^-19 |c|.  Two neighbours are trusted from a difference of
+// 2^-18 (2^-16 for a softmax) times 1 + |c| on: their errors together are at most 2^-20 (2^-18) and 31
+// of the 32 parts of 2^-23 |c|.  A group's score, of one choice or of two, is off by at most 2^-18
+// (2^-16) times 1 + its choices' magnitudes: the sum of their errors and its own rounding, 2^-24.
+// Lane first_lane + k gets pick k in id.
 template <int KPL>
 __device__ __forceinline__ bool quick_picks(const RouteArgs& a, const float (&x)[KPL], uint32_t e0, uint32_t first_lane, float& top,
                                             double& denominator, int& id) {
@@ -300,45 +310,20 @@ __device__ __forceinline__ bool quick_picks(const RouteArgs& a, const float (&x)
     }
     bool sure = true;
     if (a.groups > 1) {
-        const uint32_t per = a.experts / a.groups, lanes = per / KPL;
-        auto score_of = [&](uint32_t best, uint32_t second) {
-            return a.group_best == 2 && second != 0 ? ordered(value_of(best) + value_of(second)) : best;
-        };
-        uint32_t mine = 0;
-        if (per % KPL == 0 && (lanes & (lanes - 1)) == 0) {
-            uint32_t best = 0, second = 0;
-#pragma unroll
-            for (int j = 0; j < KPL; j++) {
-                second = max(second, min(best, key[j]));
-                best = max(best, key[j]);
-            }
-            for (uint32_t d = 1; d < lanes; d <<= 1) {
-                const uint32_t other = __shfl_xor_sync(kFull, best, d), other2 = __shfl_xor_sync(kFull, second, d);
-                second = max(min(best, other), max(second, other2));
-                best = max(best, other);
-            }
-            mine = __shfl_sync(kFull, score_of(best, second), lane * lanes);
-        } else {
-            for (uint32_t g = 0; g < a.groups; g++) {
-                uint32_t best, second;
-                best_of_group<KPL>(key, e0 - g * per, per, best, second);
-                if (lane == g) mine = score_of(best, second);
-            }
-        }
-        uint32_t above = 0;
-        for (uint32_t g = 0; g < a.groups; g++) {
-            const uint32_t other = __shfl_sync(kFull, mine, g);
-            above += other > mine || (other == mine && g < lane);
-        }
-        const bool inside = lane < a.groups, keep = inside && above < a.top_groups;
-        const uint32_t kept = __ballot_sync(kFull, keep);
-        const uint32_t low = __reduce_min_sync(kFull, keep ? mine : 0xffffffffu);
-        const uint32_t high = warp_max(inside && !keep ? mine : 0u);
-        if (high != 0) {
-            const float l = value_of(low), h = value_of(high);
-            sure = l - h > 2.0f * tolerance * (1.0f + fabsf(h));
-        }
-        drop_groups<KPL>(a, key, e0, per, kept);
+        uint32_t best, second;
+        best_of_groups<KPL>(a, key, e0, best, second);
+        const bool two = a.group_best == 2 && second != 0;
+        const float first_choice = value_of(best), second_choice = two ? value_of(second) : 0.0f;
+        const float score = first_choice + second_choice;
+        const uint32_t mine = two ? ordered(score) : best, kept = kept_groups(a, mine);
+        // A score is off by its terms' errors, which go by the terms: a sum may cancel.  The kept
+        // groups' lowest possible scores have to be above the others' highest.
+        const float error = tolerance * (1.0f + fabsf(first_choice) + fabsf(second_choice));
+        const bool counts = lane < a.groups && mine != 0, keep = (kept >> lane) & 1u;
+        const uint32_t low = __reduce_min_sync(kFull, counts && keep ? ordered(score - error) : 0xffffffffu);
+        const uint32_t high = warp_max(counts && !keep ? ordered(score + error) : 0u);
+        sure = __all_sync(kFull, !counts || error < INFINITY) && low > high;
+        drop_groups<KPL>(a, key, e0, kept);
     }
     float last = 0.0f;
     for (uint32_t k = 0; k <= a.topk; k++) {  // one more than is picked: the last must stand clear too
