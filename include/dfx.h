@@ -394,7 +394,8 @@ int dfx_route(dfx_plan_t plan, const void *d_logits, uint32_t logits_type, uint6
  *     row r as it was; one of x_rows or more does too, and sets DFX_STATUS_INDEX.  NULL needs
  *     rows <= x_rows.
  *   flags: DFX_QUANT_SWIGLU: a row of x holds cols gates, then cols values, and
- *     gate / (1 + exp(-gate)) * value is quantized (in FP32, without a rounding in between).
+ *     gate / (1 + exp(-gate)) * value is quantized (in FP32, without a rounding in between; a
+ *     product beyond FP32's range is an infinity).
  *   d_q, ld_q: rows x cols bytes; d_scales, ld_scales: ceil(rows / block_rows) x ceil(cols / 128).
  * d_index and flags go with block_rows = 1 only (else DFX_ERR_UNSUPPORTED). */
 #define DFX_QUANT_SWIGLU 0x1u

@@ -158,13 +158,14 @@ __device__ __forceinline__ float block_max(unsigned mask, float m) {
 
 // Within 2^-15 of the border the scale is settled in 64 bits, so that it does not hang on the
 // exponential's last places (one block in some 16 thousand); the n gates and values of this lane
-// are read again.
+// are read again.  The FP32 maximum is next to a border, at most 1.75 * 2^127, so what is above 1.875 *
+// 2^127 is a product that FP32 did not hold: it became NaN and has no part in the scale.
 template <class T>
 __device__ __noinline__ uint32_t swiglu_scale_64(unsigned mask, const T* gates, const T* values, uint32_t n) {
     double w = 0.0;
     for (uint32_t j = 0; j < n; j++) {
         const double v = fabs(silu_times_64(as_f32(gates[j]), as_f32(values[j])));
-        if (v < (double)INFINITY) w = fmax(w, v);
+        if (v < 0x1.ep127) w = fmax(w, v);
     }
 #pragma unroll
     for (int e = kRowLanes / 2; e > 0; e >>= 1) w = fmax(w, __shfl_xor_sync(mask, w, e));

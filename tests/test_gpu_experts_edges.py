@@ -1,9 +1,11 @@
-"""The expert-layer operators where FP32 runs out: choices that cancel."""
+"""The expert-layer operators where FP32 runs out: choices that cancel, products beyond its range."""
+import numpy as np
 import pytest
 import torch
 
 import lossless_entropy_coded_exponent_b200 as dfx
 from lossless_entropy_coded_exponent_b200 import build as dfx_build
+from test_gpu_fp8 import quantize, reference, same_bytes, to_e4m3
 from test_gpu_route import check
 
 pytestmark = pytest.mark.gpu
@@ -55,3 +57,37 @@ def test_near_group_scores_keep_their_order(plan):
     s = 1 / (1 + torch.exp(-x[0].double()))
     check(plan, x, 6, sigmoid=True, bias=(1.0 - s).float(), groups=16, top_groups=5, best=2)
     check(plan, x, 6, sigmoid=True, bias=(1.0 - s).float(), groups=16, top_groups=5, best=1)
+
+
+# ---------------------------------------------------------------- SwiGLU at the ends of FP32's range
+
+@pytest.mark.parametrize("value", [10.0, 3e38])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_swiglu_product_beyond_fp32_has_no_part_in_the_scale(plan, value, dtype):
+    """The block's largest finite product stands on the border (1.75 * 2^5), where the scale is settled in 64 bits."""
+    x = torch.zeros(3, 256)
+    x[:, 5], x[:, 128 + 5] = 56.0, 1.0
+    x[:, 9], x[:, 128 + 9] = 40.0, 0.5
+    x[0, 77], x[0, 128 + 77] = 2e38, value
+    x[1, 3], x[1, 128 + 3] = 2e38, -value
+    q, s = quantize(plan, x.to(dtype).cuda(), 3, 128, flags=dfx.DFX_QUANT_SWIGLU)
+    v = np.zeros((3, 128))
+    v[:, 5], v[:, 9] = 56.0, 20.0
+    v[0, 77] = v[1, 3] = np.nan
+    ref_s, ref_q = reference(v, 1)
+    assert np.array_equal(s, ref_s)
+    assert same_bytes(q, to_e4m3(ref_q))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_swiglu_product_beyond_fp32_beside_the_highest_border(plan, dtype):
+    """The largest product that FP32 holds is 1.75 * 2^127, the one beside it just past FP32's largest value."""
+    x = torch.zeros(2, 256)
+    x[:, 5], x[:, 128 + 5] = 1.75 * 2.0 ** 100, 2.0 ** 27
+    x[0, 77], x[0, 128 + 77] = 2e38, 1.75
+    q, s = quantize(plan, x.to(dtype).cuda(), 2, 128, flags=dfx.DFX_QUANT_SWIGLU)
+    v = np.zeros((2, 128))
+    v[:, 5], v[0, 77] = 1.75 * 2.0 ** 127, np.nan
+    ref_s, ref_q = reference(v, 1)
+    assert np.array_equal(s, ref_s)
+    assert same_bytes(q, to_e4m3(ref_q))
