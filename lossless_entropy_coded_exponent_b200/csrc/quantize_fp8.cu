@@ -127,7 +127,9 @@ __device__ __forceinline__ float reciprocal_fast(float x) {
 
 // gate / (1 + exp(-gate)) * value of eight neighbours: with the approximate power of two and
 // reciprocal (together within 2^-22 + |gate| 2^-24) unless a gate is so low that 1 + exp(-gate)
-// leaves the reciprocal's range
+// leaves the reciprocal's range.  Below -88.7 it leaves FP32's, where a large value still makes a product
+// that FP32 holds: from -80 down the quotient is gate * exp(-80) * exp(gate + 80), of which the
+// last factor comes in two halves behind the value (within 2^-20)
 __device__ __forceinline__ void swiglu(const float (&g)[8], const float (&u)[8], float (&v)[8]) {
     float low = g[0];
 #pragma unroll
@@ -144,7 +146,11 @@ __device__ __forceinline__ void swiglu(const float (&g)[8], const float (&u)[8],
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
+        for (int i = 0; i < 8; i++) {
+            constexpr float kExpMinus80 = 1.8048513878454153e-35f;
+            const float half = expf(0.5f * fminf(g[i] + 80.0f, 0.0f));
+            v[i] = (g[i] > -80.0f ? g[i] / (1.0f + expf(-g[i])) : g[i] * kExpMinus80) * u[i] * half * half;
+        }
     }
 }
 __device__ __forceinline__ double silu_times_64(float g, float u) { return (double)g / (1.0 + exp(-(double)g)) * (double)u; }

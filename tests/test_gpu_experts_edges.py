@@ -1,4 +1,5 @@
-"""The expert-layer operators where FP32 runs out: choices that cancel, products beyond its range."""
+"""The expert-layer operators where FP32 runs out: choices that cancel, products beyond its range,
+gates so low that their exponential is."""
 import numpy as np
 import pytest
 import torch
@@ -91,3 +92,27 @@ def test_swiglu_product_beyond_fp32_beside_the_highest_border(plan, dtype):
     ref_s, ref_q = reference(v, 1)
     assert np.array_equal(s, ref_s)
     assert same_bytes(q, to_e4m3(ref_q))
+
+
+@pytest.mark.parametrize("cols", [1, 8])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_swiglu_of_low_gates(plan, cols, dtype):
+    """Gates whose exp(-gate) is beyond FP32, beside values large enough for a product that is not."""
+    gates = torch.linspace(-200.0, -70.0, 131)
+    factors = torch.tensor([1.0, 1e6, -1e10, 1e20, -1e30, 1e38, 3e38])
+    g, u = gates.repeat_interleave(7).to(dtype), factors.repeat(131).to(dtype)
+    x = torch.cat([g[:, None].repeat(1, cols), u[:, None].repeat(1, cols)], 1)
+    q, s = quantize(plan, x.cuda(), x.shape[0], cols, flags=dfx.DFX_QUANT_SWIGLU)
+    gd, ud = x[:, :cols].double().numpy(), x[:, cols:].double().numpy()
+    v = gd / (1 + np.exp(-gd)) * ud
+    ref_s, ref_q = reference(v, 1)
+    normal = np.abs(v[:, 0]) >= 2.0 ** -126  # FP32 holds it in full
+    assert 0 < normal.sum() < normal.size
+    assert np.array_equal(s[normal], ref_s[normal])
+    got = torch.from_numpy(q).view(torch.float8_e4m3fn).double().numpy()
+    # half a step of e4m3 (2^-4 of the value, 2^-10 among its subnormals), FP32's rounding of the product (2^-24)
+    assert np.all(np.abs(got - ref_q)[normal] <= (np.abs(ref_q) * (2.0 ** -4 + 2.0 ** -20) + 2.0 ** -10)[normal])
+    # below: FP32 rounds the product to a multiple of 2^-149
+    rest = ~normal
+    held = got * np.ldexp(1.0, s[:, :1].astype(np.int64) - 127)
+    assert np.all(np.abs(held - v)[rest] <= (np.abs(v) * (2.0 ** -4 + 2.0 ** -20) + 2.0 ** -137)[rest])
