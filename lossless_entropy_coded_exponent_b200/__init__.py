@@ -597,6 +597,14 @@ def experts_fp8(x, logits, w_in: Fp8, w_out: Fp8, topk: int, plan: Plan | None =
       [experts, width, inner]; routing: route's keywords.  The result has x's type."""
     import torch
 
+    if x.dim() != 2 or logits.dim() != 2 or x.shape[0] != logits.shape[0]:
+        raise ValueError("experts_fp8: x [tokens, width] and logits [tokens, experts] of the same tokens")
+    for w, shape in ((w_in, (2 * w_out.cols, x.shape[1])), (w_out, (x.shape[1], w_out.cols))):
+        _whole_fp8(w, "experts_fp8")
+        if w.block_rows != 128 or w.values.dim() not in (2, 3) or (w.values.shape[-2], w.cols) != shape \
+                or w.values.shape[:-2].numel() != logits.shape[1]:
+            raise ValueError("experts_fp8: w_in [experts, 2 * inner, width] and w_out [experts, width, inner] in blocks of "
+                             "128 rows, a matrix for each column of logits")
     _same_device("experts_fp8", x, logits, w_in.values, w_out.values)
     with _call(x, plan, stream, "experts_fp8") as (p, _):
         r = route(logits, topk, plan=p, **routing)

@@ -1,0 +1,44 @@
+"""What the tensor helpers of the expert layers refuse before they touch a device."""
+import pytest
+import torch
+
+import lossless_entropy_coded_exponent_b200 as dfx
+
+
+def weight(*shape, block_rows=128):
+    """An Fp8 of shape [.., rows, cols]."""
+    *lead, rows, cols = shape
+    up = lambda n, to: -(-n // to) * to  # noqa: E731
+    return dfx.Fp8(torch.zeros(*lead, rows, up(cols, 16), dtype=torch.uint8),
+                   torch.zeros(*lead, -(-rows // block_rows), up(-(-cols // 128), 16), dtype=torch.uint8), cols, block_rows)
+
+
+LAYER = dict(x=torch.zeros(10, 200), logits=torch.zeros(10, 4), w_in=weight(4, 96, 200), w_out=weight(4, 200, 48), topk=2)
+
+
+def test_a_sound_layer_is_only_stopped_by_the_missing_device():
+    with pytest.raises(ValueError, match="CUDA device"):
+        dfx.experts_fp8(**LAYER)
+    with pytest.raises(ValueError, match="CUDA device"):  # one matrix for one expert
+        dfx.experts_fp8(**{**LAYER, "logits": torch.zeros(10, 1), "w_in": weight(96, 200), "w_out": weight(200, 48), "topk": 1})
+
+
+@pytest.mark.parametrize("changes", [
+    dict(logits=torch.zeros(9, 4)),            # fewer tokens than x: rows of the result would be missing
+    dict(logits=torch.zeros(11, 4)),           # more: rows that x does not have
+    dict(logits=torch.zeros(4)),
+    dict(x=torch.zeros(1, 10, 200)),
+    dict(x=torch.zeros(10, 199)),
+    dict(logits=torch.zeros(10, 5)),           # an expert without a matrix
+    dict(logits=torch.zeros(10, 3)),
+    dict(w_in=weight(4, 98, 200)),             # gates and values of other widths than w_out's
+    dict(w_out=weight(4, 200, 47)),
+    dict(w_out=weight(4, 199, 48)),
+    dict(w_out=weight(3, 200, 48)),
+    dict(w_in=weight(96, 200)),
+    dict(w_in=weight(2, 2, 96, 200)),
+    dict(w_in=weight(4, 96, 200, block_rows=1)),
+])
+def test_layers_whose_parts_do_not_fit_are_refused(changes):
+    with pytest.raises(ValueError, match="experts_fp8: (x|w_in)"):
+        dfx.experts_fp8(**{**LAYER, **changes})
