@@ -420,6 +420,8 @@ def _call(tensor, plan, stream, what):
 
     if not tensor.is_cuda:
         raise ValueError(f"{what}: tensors must be on a CUDA device (there is no CPU fallback)")
+    if stream is not None and stream.device != tensor.device:
+        raise ValueError(f"{what}: a stream of {stream.device} for tensors on {tensor.device}")
     with torch.cuda.device(tensor.device), torch.cuda.stream(stream):
         handle = torch.cuda.current_stream().cuda_stream
         own = plan is None

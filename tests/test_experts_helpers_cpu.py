@@ -1,4 +1,6 @@
 """What the tensor helpers of the expert layers refuse before they touch a device."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -42,3 +44,29 @@ def test_a_sound_layer_is_only_stopped_by_the_missing_device():
 def test_layers_whose_parts_do_not_fit_are_refused(changes):
     with pytest.raises(ValueError, match="experts_fp8: (x|w_in)"):
         dfx.experts_fp8(**{**LAYER, **changes})
+
+
+class Elsewhere(torch.Tensor):
+    """Only claims its device."""
+    is_cuda, device = True, torch.device("cuda", 0)
+
+
+def elsewhere(t):
+    if isinstance(t, dfx.Fp8):
+        return t._replace(values=elsewhere(t.values), scales=elsewhere(t.scales))
+    return t.as_subclass(Elsewhere)
+
+
+@pytest.mark.parametrize("helper,args", [
+    ("route", (torch.zeros(4, 8), 2)),
+    ("quantize_fp8", (torch.zeros(4, 8),)),
+    ("gemm_fp8", (weight(4, 128, block_rows=1), weight(4, 128))),
+    ("combine", (torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2))),
+    ("experts_fp8", tuple(LAYER.values())),
+])
+def test_a_stream_of_another_device_is_refused(helper, args, monkeypatch):
+    """Its kernels would get addresses of a device that is not theirs."""
+    monkeypatch.setattr(dfx, "dfx_plan", lambda n: pytest.fail("the call went on"))
+    args = [a if isinstance(a, int) else elsewhere(a) for a in args]
+    with pytest.raises(ValueError, match="a stream of cuda:1"):
+        getattr(dfx, helper)(*args, stream=SimpleNamespace(device=torch.device("cuda", 1)))
