@@ -391,8 +391,9 @@ def decode(comp, n: int, plan: Plan | None = None, out=None, stream=None, check:
 
 
 # Layers of experts with 8-bit weights.  These run on the tensors' device and on its current
-# torch stream (or `stream`, a torch stream: then what they allocate belongs to it).  A plan of
-# the device may be passed in; without one a call makes its own, waits for the work and raises
+# torch stream (or `stream`, a torch stream: then what they allocate belongs to it, and the memory of
+# their tensors is not given to others before its work on them is done; the caller lets it wait for
+# the work that makes them).  A plan of the device may be passed in; without one a call makes its own, waits for the work and raises
 # if its status word says that an index was out of range or a wait ran out.
 
 class Fp8(NamedTuple):
@@ -414,15 +415,21 @@ class Routing(NamedTuple):
 
 
 @contextlib.contextmanager
-def _call(tensor, plan, stream, what):
-    """Device, stream and plan of a helper's calls: yields (plan, stream handle)."""
+def _call(tensors, plan, stream, what):
+    """Device, stream and plan of a helper's calls on `tensors` (or None among them): yields
+    (plan, stream handle)."""
     import torch
 
+    tensor = tensors[0]
     if not tensor.is_cuda:
         raise ValueError(f"{what}: tensors must be on a CUDA device (there is no CPU fallback)")
     if stream is not None and stream.device != tensor.device:
         raise ValueError(f"{what}: a stream of {stream.device} for tensors on {tensor.device}")
     with torch.cuda.device(tensor.device), torch.cuda.stream(stream):
+        if stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
         handle = torch.cuda.current_stream().cuda_stream
         own = plan is None
         if own:
@@ -491,7 +498,7 @@ def route(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1,
         raise ValueError("route: score is 'softmax' or 'sigmoid'")
     kind = _float_type(logits.dtype, "route")
     _same_device("route", logits, bias)
-    with _call(logits, plan, stream, "route") as (p, s):
+    with _call((logits, bias), plan, stream, "route") as (p, s):
         x = _matrix(logits, "route")
         tokens, experts = x.shape
         if bias is not None:
@@ -527,7 +534,7 @@ def quantize_fp8(x, block_rows: int = 1, index=None, swiglu: bool = False, plan:
     cols = x.shape[-1] // 2 if swiglu else x.shape[-1]
     rows = x.shape[-2] if index is None else index.numel()
     blocks = -(-cols // 128)
-    with _call(x, plan, stream, "quantize_fp8") as (p, s):
+    with _call((x, index), plan, stream, "quantize_fp8") as (p, s):
         q = torch.empty(*x.shape[:-2], rows, -(-cols // 16) * 16, dtype=torch.uint8, device=x.device)
         # rows of scales in 16-byte pieces, which the product loads faster
         sc = torch.empty(*x.shape[:-2], -(-rows // block_rows), -(-blocks // 16) * 16, dtype=torch.uint8, device=x.device)
@@ -563,7 +570,7 @@ def gemm_fp8(x: Fp8, w: Fp8, offsets=None, dtype=None, out=None, plan: Plan | No
         raise ValueError("gemm_fp8: out is a [tokens, rows] matrix with neighbouring elements")
     dtype = out.dtype if out is not None else dtype or torch.bfloat16
     kind = _float_type(dtype, "gemm_fp8")
-    with _call(x.values, plan, stream, "gemm_fp8") as (p, s):
+    with _call((*x[:2], *w[:2], offsets, out), plan, stream, "gemm_fp8") as (p, s):
         tokens, rows = x.values.shape[0], w.values.shape[-2]
         y = torch.empty(tokens, rows, dtype=dtype, device=x.values.device) if out is None else out
         dfx_gemm_fp8(p, x.values, x.values.shape[-1], x.scales, x.scales.shape[-1], tokens, w.values, w.values.shape[-1],
@@ -581,7 +588,7 @@ def combine(z, slots, weights, dtype=None, plan: Plan | None = None, stream=None
     if slots.shape != weights.shape or slots.dim() != 2 or slots.dtype != torch.int32 or weights.dtype != torch.float32:
         raise ValueError("combine: int32 slots and float32 weights [tokens, topk]")
     _same_device("combine", z, slots, weights)
-    with _call(z, plan, stream, "combine") as (p, s):
+    with _call((z, slots, weights), plan, stream, "combine") as (p, s):
         m = _matrix(z, "combine")
         slots, weights = (t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=_contiguous())
                           for t in (slots, weights))
@@ -608,7 +615,7 @@ def experts_fp8(x, logits, w_in: Fp8, w_out: Fp8, topk: int, plan: Plan | None =
             raise ValueError("experts_fp8: w_in [experts, 2 * inner, width] and w_out [experts, width, inner] in blocks of "
                              "128 rows, a matrix for each column of logits")
     _same_device("experts_fp8", x, logits, w_in.values, w_out.values)
-    with _call(x, plan, stream, "experts_fp8") as (p, _):
+    with _call((x, logits, *w_in[:2], *w_out[:2], routing.get("bias")), plan, stream, "experts_fp8") as (p, _):
         r = route(logits, topk, plan=p, **routing)
         # the tokens in the experts' order, an expert's rows beside one another
         xq = quantize_fp8(x, index=r.rows, plan=p)
