@@ -294,7 +294,8 @@ int dfx_device_status(dfx_plan_t plan, cudaStream_t stream, uint32_t *h_status);
  * in flight.  flags = 0 restores normal decoding.  Process-wide, not for
  * concurrent use; unknown flags return DFX_ERR_ARG. */
 #define DFX_INJECT_SKIP_SLICE_COPY 0x1u
-/* The same for dfx_gemm_fp8: every later call leaves out each CTA's first tile copies. */
+/* The same for dfx_gemm_fp8: every later call leaves out each CTA's tile copies from the middle of
+ * its first unit of work on (all of them where that is one block of columns). */
 #define DFX_INJECT_SKIP_TILE_COPY 0x4u
 int dfx_debug_inject(uint32_t flags);
 

@@ -34,8 +34,8 @@
 //         neighbours), which tcgen05.cp spreads over the lanes;
 //   4-7, 4-11 for up to 128 tokens: read the accumulator (lane = row of W) and write Y, while the
 //         next unit's MMAs run into the other accumulator.
-// Every wait is bounded: one that runs out sets DFX_STATUS_TIMEOUT, the CTA's warps leave their
-// loops, and the copies and MMAs in flight are waited for before the tensor memory is freed.
+// Every wait is bounded: one that runs out sets DFX_STATUS_TIMEOUT and the CTA's warps leave their
+// loops.  On every way out the copies and MMAs in flight are waited for before the tensor memory is freed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -414,14 +414,16 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ tiles
         uint32_t st = 0, ph = 0, issued = 0;
-        bool ok = a.g.inject == 0;  // test hook: the copies are left out
+        bool ok = true;
+        // test hook: the copies from the middle of the first unit on are left out
+        const uint32_t kb_stop = a.g.inject ? (kb_begin + kb_end) / 2 : kb_end;
         for (uint32_t u = first; ok && u < units; u += step) {
             const Unit w = walk.uniform(u);
             // this CTA's tokens: all, or its half of the columns
             const uint32_t held = w.columns / S::kCtas, token = w.first + rank * held;
             const uint32_t boxes = (held + S::kBox - 1) / S::kBox;
             const uint32_t row = w.expert * a.g.rows + (w.row_unit * S::kCtas + rank) * kTileRows;
-            for (uint32_t kb = kb_begin; kb < kb_end; kb++) {
+            for (uint32_t kb = kb_begin; kb < kb_stop; kb++) {
                 if (issued >= S::kStages && !(ok = wait(&bar_free[st], ph ^ 1u))) break;
                 const uint32_t sA = tiles + st * S::kStageBytes, sB = sA + kABytes;
                 const uint32_t bar = first_cta<P>(&bar_full[st]);
@@ -435,18 +437,20 @@ __global__ void __launch_bounds__(S::kThreads, 1)
                 issued++;
                 if (++st == S::kStages) st = 0, ph ^= 1u;
             }
+            ok = ok && kb_stop == kb_end;
         }
-        if (!ok && issued) {
-            // the copies in flight land before the CTA ends: those of each stage's last use, or,
-            // where their barrier is the other CTA's, within a thousand times their usual time
-            if constexpr (P) {
-                for (uint32_t i = 0; i < 1000; i++) __nanosleep(1000);
-            } else {
-                for (uint32_t i = 0; i < S::kStages && i < issued; i++) {
-                    const uint32_t last = issued - 1 - i;
-                    mbar_wait(&bar_full[last % S::kStages], (last / S::kStages) & 1u);
-                }
+        // The copies in flight land before the CTA ends, also when it was another warp that gave up:
+        // those of each stage's last use (of a pair both CTAs', which end together).
+        if (rank == 0)
+            for (uint32_t i = 0; i < S::kStages && i < issued; i++) {
+                const uint32_t last = issued - 1 - i;
+                mbar_wait(&bar_full[last % S::kStages], (last / S::kStages) & 1u);
             }
+        // of a pair that stopped half-way one CTA may have begun copies that the other did not expect:
+        // a millisecond is a thousand times what they take
+        if (P && !ok) {
+            const long long begin = clock64();
+            for (uint32_t i = 0; i < (1u << 20) && clock64() - begin < 2000000; i++) __nanosleep(1000);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
@@ -495,13 +499,14 @@ __global__ void __launch_bounds__(S::kThreads, 1)
                     __syncwarp();
                     if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
                 }
-                // the accumulator is ready; after a wait that ran out, what was issued completes
-                // before the tensor memory is freed
+                // the accumulator is ready
                 if (elect_one()) commit<P>(&bar_acc[acc]);
                 __syncwarp();
-                if (!ok) mbar_wait(&bar_acc[acc], acc_ph);
                 if (++acc == S::kAccs) acc = 0, acc_ph ^= 1u;
             }
+            // what was issued completes before the tensor memory is freed, also when the warps that read it
+            // have given up
+            if (unit) mbar_wait(&bar_acc[acc ? acc - 1 : S::kAccs - 1], acc ? acc_ph : acc_ph ^ 1u);
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ scales
