@@ -419,7 +419,7 @@ int dfx_quantize_fp8(dfx_plan_t plan, const void *d_x, uint32_t x_type, uint64_t
  *     An offset out of order or range is clamped and sets DFX_STATUS_INDEX.
  *   d_y, y_type, ld_y: tokens x rows, DFX_F32 or DFX_BF16, ld_y elements apart; the elements of
  *     a row behind `rows` stay as they were.
- * experts <= 1024 (else DFX_ERR_UNSUPPORTED); tokens and experts * rows < 2^31 (else
+ * experts <= 1024 (else DFX_ERR_UNSUPPORTED); tokens and experts * rows < 2^31, cols <= 2^25 (else
  * DFX_ERR_TOO_LARGE).  A wait inside the kernel that runs out sets DFX_STATUS_TIMEOUT (Y is then
  * not valid).  One launch. */
 int dfx_gemm_fp8(dfx_plan_t plan, const void *d_x, uint64_t ld_x, const void *d_x_scales, uint64_t ld_x_scales,

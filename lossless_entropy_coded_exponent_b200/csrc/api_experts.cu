@@ -134,7 +134,7 @@ int dfx_gemm_fp8(dfx_plan_t plan, const void* d_x, uint64_t ld_x, const void* d_
     if (!plan || !float_type(y_type) || experts == 0 || cols == 0) return DFX_ERR_ARG;
     if (experts > 1 && !d_offsets) return DFX_ERR_ARG;
     if (experts > dfx::kMaxGemmExperts) return DFX_ERR_UNSUPPORTED;
-    if (tokens >= (1ull << 31) || cols >= (1ull << 31) || rows >= (1ull << 31) || rows * experts >= (1ull << 31))
+    if (tokens >= (1ull << 31) || cols > dfx::kMaxGemmCols || rows >= (1ull << 31) || rows * experts >= (1ull << 31))
         return DFX_ERR_TOO_LARGE;
     const uint64_t blocks = (cols + dfx::kScaleBlock - 1) / dfx::kScaleBlock;
     if (ld_x < cols || ld_x % 16 != 0 || ld_w < cols || ld_w % 16 != 0 || ld_y < rows) return DFX_ERR_ARG;

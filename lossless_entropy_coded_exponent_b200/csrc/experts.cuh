@@ -14,6 +14,9 @@ constexpr uint32_t kMaxExperts = 512;        // of a router
 constexpr uint32_t kMaxTopk = 32;            // experts per token
 constexpr uint32_t kMaxRouteGroups = 32;     // groups of experts
 constexpr uint32_t kMaxGemmExperts = 1024;   // matrices of one grouped product
+// columns of a product: a sum over 2^25 of them takes 0.1 s and more, and the warps that wait for it give up
+// after some 0.35 s
+constexpr uint64_t kMaxGemmCols = 1ull << 25;
 
 struct RouteArgs {
     const void* logits;

@@ -1,10 +1,11 @@
-"""What the tensor helpers of the expert layers refuse before they touch a device."""
+"""What the expert-layer calls and their tensor helpers refuse before they touch a device."""
 from types import SimpleNamespace
 
 import pytest
 import torch
 
 import lossless_entropy_coded_exponent_b200 as dfx
+from lossless_entropy_coded_exponent_b200 import build as dfx_build
 
 
 def weight(*shape, block_rows=128):
@@ -70,3 +71,14 @@ def test_a_stream_of_another_device_is_refused(helper, args, monkeypatch):
     args = [a if isinstance(a, int) else elsewhere(a) for a in args]
     with pytest.raises(ValueError, match="a stream of cuda:1"):
         getattr(dfx, helper)(*args, stream=SimpleNamespace(device=torch.device("cuda", 1)))
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="passes a plan and pointers that are not the device's")
+def test_sums_too_long_for_the_waits_are_refused():
+    """The warps that wait for a sum over K give up after some 0.35 s, and 128 columns take some 0.4 us."""
+    from test_experts_cpu import CUDA, GEMM, TOO_LARGE, call
+
+    dfx_build.build()
+    for cols, code in ((1 << 25, CUDA), ((1 << 25) + 1, TOO_LARGE), (1 << 30, TOO_LARGE)):
+        ld, blocks = -(-cols // 16) * 16, -(-cols // 512) * 4
+        assert call("dfx_gemm_fp8", GEMM, cols=cols, ld_x=ld, ld_w=ld, ld_sx=blocks, ld_sw=blocks) == code
