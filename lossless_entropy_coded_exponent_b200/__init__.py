@@ -614,8 +614,9 @@ def experts_fp8(x, logits, w_in: Fp8, w_out: Fp8, topk: int, plan: Plan | None =
                 or w.values.shape[:-2].numel() != logits.shape[1]:
             raise ValueError("experts_fp8: w_in [experts, 2 * inner, width] and w_out [experts, width, inner] in blocks of "
                              "128 rows, a matrix for each column of logits")
-    _same_device("experts_fp8", x, logits, w_in.values, w_out.values)
-    with _call((x, logits, *w_in[:2], *w_out[:2], routing.get("bias")), plan, stream, "experts_fp8") as (p, _):
+    tensors = (x, logits, *w_in[:2], *w_out[:2], routing.get("bias"))
+    _same_device("experts_fp8", *tensors)
+    with _call(tensors, plan, stream, "experts_fp8") as (p, _):
         r = route(logits, topk, plan=p, **routing)
         # the tokens in the experts' order, an expert's rows beside one another
         xq = quantize_fp8(x, index=r.rows, plan=p)

@@ -73,6 +73,19 @@ def test_a_stream_of_another_device_is_refused(helper, args, monkeypatch):
         getattr(dfx, helper)(*args, stream=SimpleNamespace(device=torch.device("cuda", 1)))
 
 
+@pytest.mark.parametrize("changes", [
+    dict(bias=torch.zeros(4)),
+    dict(logits=LAYER["logits"]),
+    dict(w_in=elsewhere(LAYER["w_in"])._replace(scales=LAYER["w_in"].scales)),
+    dict(w_out=elsewhere(LAYER["w_out"])._replace(values=LAYER["w_out"].values)),
+])
+@pytest.mark.parametrize("stream", [None, SimpleNamespace(device=torch.device("cuda", 0))])
+def test_a_layer_on_several_devices_is_refused(changes, stream):
+    layer = {k: v if isinstance(v, int) else elsewhere(v) for k, v in LAYER.items()}
+    with pytest.raises(ValueError, match="different devices"):
+        dfx.experts_fp8(**{**layer, **changes}, stream=stream)
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="passes a plan and pointers that are not the device's")
 def test_sums_too_long_for_the_waits_are_refused():
     """The warps that wait for a sum over K give up after some 0.35 s, and 128 columns take some 0.4 us."""
