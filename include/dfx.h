@@ -372,7 +372,8 @@ int dfx_route_workspace(uint64_t tokens, uint32_t experts, const dfx_route_param
  * scores sum to 0, renormalised weights are 0.
  *   d_logits, logits_type, ld_logits: tokens x experts, DFX_F32 or DFX_BF16, rows ld_logits
  *     elements apart; experts <= 512 (else DFX_ERR_UNSUPPORTED).  d_bias: NULL or FP32[experts].
- *   d_ids, d_weights: tokens x topk, best first.
+ *   d_ids, d_weights: tokens x topk, best first.  Weights are formed in FP64 and rounded once, but for a
+ *     softmax that is not renormalized, whose sum over all logits is formed in FP32 (within 2^-18).
  *   d_offsets: int32[experts + 1]; d_rows: int32[tokens * topk]; d_slots: int32[tokens x topk];
  *     or all NULL.  The assignments of expert e have the slots offsets[e] .. offsets[e + 1] - 1
  *     in the order of their tokens; rows[slot] is the token, slots[t, k] the slot of a token's

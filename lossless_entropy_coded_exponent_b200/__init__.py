@@ -491,7 +491,8 @@ def _same_device(what: str, *tensors):
 def route(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
           group_best: int = 1, renormalize: bool = False, scale: float = 1.0, plan: Plan | None = None,
           stream=None) -> Routing:
-    """Each token's best experts (dfx_route) from gate logits [tokens, experts]."""
+    """Each token's best experts (dfx_route) from gate logits [tokens, experts].  scale: a factor of
+    every weight (0 counts as 1)."""
     import torch
 
     if score not in ("softmax", "sigmoid"):

@@ -17,13 +17,13 @@
 //   up to 32 and up to 128 tokens on one CTA.  Bound by DRAM: 128 rows to 128 experts of
 //     2048 x 4096 in 112 to 117 us (6.0 to 6.25 TB/s, 93 to 97 % of the measured copy rate).
 //     Where units are few, the CTAs of a cluster share a unit's K and add their sums up through
-//     distributed shared memory, in the order of K's parts: one token through 4096 x 4096 in
-//     7.1 us (10.4 unsplit), through 4096 x 14336 in 14.7 us (29);
+//     distributed shared memory, in the order of K's parts: one token through 4096 x 14336 in
+//     14.5 us (29 unsplit), 16 tokens through 4096 x 4096 in 7.2 us;
 //   up to 240 (256) tokens on a pair of CTAs (cta_group::2), each holding 128 rows of W and half of
 //     the tokens, which halves the shared-memory traffic of a product that the cores bound:
-//     8192 tokens through 14336 x 4096 in 375 us while the clock holds (2.6 PFLOP/s; 560 cycles
-//     a block, of which the MMAs take 490), 430 us once the power limit has it (the MMAs alone
-//     without copies or stores: 260 us).
+//     8192 tokens through 14336 x 4096 take some 500 thousand cycles (27 waves of 32 blocks, 577 a
+//     block, of which the MMAs take 490): 362 us in a short run (2.66 PFLOP/s), 431 us once the
+//     power limit holds the clock at 1.16 GHz (the MMAs alone without copies or stores: 260 us).
 // A persistent CTA (pair) takes units in turn.  Warps:
 //   0     brings the tiles in by TMA (128-byte swizzle), kStages deep;
 //   1     issues the MMAs and copies each group of four blocks' scale bytes from shared to

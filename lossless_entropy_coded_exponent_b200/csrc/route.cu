@@ -24,7 +24,7 @@
 //
 // Bound by instructions and their latency, not by memory: 32749 tokens over 128 experts, 8 each, in
 // 25 us (2 us for their bytes), of which k_route takes 14.6; 4096 over 256 in 8 groups with a bias in
-// 20 (13.3; 29 with every choice in FP64).
+// 20.6 (13.3; 29 with every choice in FP64).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -398,7 +398,10 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, uint32_t t0, ui
         }
     }
 
-    // the weights, in FP64 and rounded once: one value per lane
+    // The weights, in FP64 and rounded once: one value per lane.  Where a softmax over all logits is the
+    // denominator, it is an FP32 sum of FP32 exponentials, within 2^-18 (exponentials of every expert in
+    // FP64 are what makes the choices in FP64 half as slow again); for a token whose choices were made in
+    // FP64 it is their sum.
     double w = 0.0;
     if (id >= 0) {
         const float chosen = logit(a, (uint64_t)(t0 + my_token) * a.ld + id);
